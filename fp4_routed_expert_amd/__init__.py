@@ -7,6 +7,9 @@ device memory and streams only.
 
     pw = prepack_weights(w1, s1, w3, s3, w2, s2)          # once, at load time
     y  = moe_layer(pw, x_bf16, logits, k)                  # route/sort/quant/experts/combine
+
+The operators around the layer (``include/moe_mx4.h``) are in ``mx4``: MXFP4
+quantisation, MXFP4 x MXFP4 products, and the norms before and after a block.
 """
 from __future__ import annotations
 
@@ -18,6 +21,9 @@ import torch
 from . import _lib
 from ._lib import (MOE_FLAG_FORCE_DECODE, MOE_FLAG_FORCE_PREFILL, MoeError,  # noqa: F401
                    MoeFp4Weights)
+from .mx4 import (Mxfp4Weights, block_forward, block_workspace_size, dequant_mx, mxfp4_dense,  # noqa: F401
+                  mxfp4_grouped, mxfp4_grouped_workspace_size, mxfp4_prepack, mxfp4_prepack_glu,
+                  norm_after, norm_before, quant_mxfp4)
 
 __all__ = [
     "route_topk", "sort_permute", "quant_act_mxfp8", "prepack_weights", "PackedWeights",
@@ -27,6 +33,9 @@ __all__ = [
     "router_workspace_size",
     "shared_workspace_size", "shared_expert", "combine_shared", "layer_full_workspace_size",
     "layer_forward_full", "DenseWeights", "dense_prepack", "dense_forward", "dense_layer",
+    "quant_mxfp4", "dequant_mx", "Mxfp4Weights", "mxfp4_prepack", "mxfp4_prepack_glu", "mxfp4_dense",
+    "mxfp4_grouped", "mxfp4_grouped_workspace_size", "norm_before", "norm_after", "block_forward",
+    "block_workspace_size",
     "MOE_FLAG_FORCE_DECODE", "MOE_FLAG_FORCE_PREFILL", "MoeError",
 ]
 

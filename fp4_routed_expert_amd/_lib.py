@@ -23,6 +23,12 @@ MOE_FLAG_FORCE_PREFILL = 2
 MOE_FP4_LAYOUT_VERSION = 1
 MOE_FP8_DENSE_LAYOUT_VERSION = 1
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
+MOE_MXFP4_LAYOUT_VERSION = 1
+
+# moe_mx4.h
+MX4_HEADER = os.path.join(os.path.dirname(HERE), "include", "moe_mx4.h")
+MOE_TYPE_BF16, MOE_TYPE_FP16, MOE_TYPE_FP32 = 0, 1, 2
+MOE_QUANT_NONE, MOE_QUANT_MXFP8, MOE_QUANT_MXFP4 = 0, 1, 2
 
 
 class MoeFp4Weights(ctypes.Structure):
@@ -46,6 +52,32 @@ class MoeFp8DenseWeights(ctypes.Structure):
     ]
 
 
+class MoeMxfp4Weights(ctypes.Structure):
+    _fields_ = [
+        ("E", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("glu", ctypes.c_int32),
+        ("layout_version", ctypes.c_uint32),
+        ("packed", ctypes.c_void_p),
+        ("packed_bytes", ctypes.c_size_t),
+    ]
+
+
+class MoeBlockNorms(ctypes.Structure):
+    _fields_ = [
+        ("w_pre", ctypes.c_void_p),
+        ("w_post", ctypes.c_void_p),
+        ("w_type", ctypes.c_int32),
+        ("gate", ctypes.c_void_p),
+        ("gate_t", ctypes.c_int64),
+        ("gate_h", ctypes.c_int64),
+        ("alpha", ctypes.c_float),
+        ("beta", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -60,6 +92,10 @@ _U32 = ctypes.c_uint32
 _SZ = ctypes.c_size_t
 _WP = ctypes.POINTER(MoeFp4Weights)
 _DP = ctypes.POINTER(MoeFp8DenseWeights)
+_MP = ctypes.POINTER(MoeMxfp4Weights)
+_BP = ctypes.POINTER(MoeBlockNorms)
+_I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -92,6 +128,21 @@ SIGNATURES = {
     "moe_fp8_dense_packed_bytes": (_SZ, [_I32, _I32]),
     "moe_fp8_dense_prepack": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _SZ, _DP, _P]),
     "moe_fp8_dense_forward": (ctypes.c_int, [_DP, _P, _P, _I32, _P, _U32, _P]),
+    # moe_mx4.h
+    "moe_quant_mxfp4": (ctypes.c_int, [_P, _I32, _I32, _I32, _I64, _P, _P, _P]),
+    "moe_dequant_mx": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _P, _I32, _P]),
+    "moe_mxfp4_packed_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "moe_mxfp4_prepack": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32, _I32, _P, _SZ, _MP, _P]),
+    "moe_mxfp4_dense_forward": (ctypes.c_int, [_MP, _P, _P, _I32, _P, _I32, _U32, _P]),
+    "moe_mxfp4_grouped_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
+    "moe_mxfp4_grouped_forward": (ctypes.c_int, [_MP, _P, _P, _I32, _P, _P, _I32, _I32, _P, _I32, _P,
+                                                 _SZ, _U32, _P]),
+    "moe_norm_before": (ctypes.c_int, [_P, _I32, _P, _I32, _I32, _I32, _F32, _P, _P, _P, _I32, _P]),
+    "moe_norm_after": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _I32, _P, _I64, _I64, _F32, _F32, _F32,
+                                      _I32, _I32, _P, _P, _P, _P, _I32, _P]),
+    "moe_fp4_block_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _U32]),
+    "moe_fp4_block_forward": (ctypes.c_int, [_WP, _I32, _P, _BP, _P, _I32, _I32, _I32, _P, _P, _SZ, _U32,
+                                             _P]),
 }
 
 

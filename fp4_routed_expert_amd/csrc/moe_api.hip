@@ -3,8 +3,9 @@
 // launch, so a failing call enqueues nothing and touches no output.
 #include <atomic>
 
+#include "api.h"
 #include "common.h"
-#include "../../include/moe_fp4.h"
+#include "mx4.h"
 
 using namespace moe;
 
@@ -12,11 +13,15 @@ namespace {
 
 thread_local int g_last_hip_error = 0;
 
+}  // namespace
+
 // Every launch records its result for moe_last_hip_error (0 on success).
-moe_status_t hip_status(hipError_t e) {
+moe_status_t moe::hip_status(hipError_t e) {
   g_last_hip_error = (int)e;
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
+
+namespace {
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -687,6 +692,96 @@ moe_status_t moe_fp8_dense_forward(const moe_fp8_dense_weights_t* w, const uint8
   const bool decode = fd || (!fp && T <= kDenseDecodeMaxT);
   if (decode) return hip_status(launch_dense_decode(pk, xq, xs, T, w->N, w->K, y, stream));
   return hip_status(launch_dense_prefill(pk, xq, xs, T, w->N, w->K, y, stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------ the layer between its norms
+namespace {
+
+// z (the normed rows), y (the layer's output) and the layer's own workspace.
+struct BlockCarve {
+  size_t z, y, full, total;
+};
+
+BlockCarve block_carve(int32_t T, int32_t k, int32_t E, int32_t H, int32_t I, int32_t ns) {
+  BlockCarve c;
+  c.z = 0;
+  c.y = align256(c.z + (size_t)T * H * 2);
+  c.full = align256(c.y + (size_t)T * H * 4);
+  c.total = align256(c.full + full_carve(T, k, E, H, I, ns).total);
+  return c;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_fp4_block_workspace_size(int32_t T, int32_t E, int32_t k, int32_t H, int32_t I,
+                                    int32_t n_shared, uint32_t flags) {
+  if (moe_fp4_layer_full_workspace_size(T, E, k, H, I, n_shared, flags) == 0) return 0;
+  return block_carve(T, k, E, H, I, n_shared).total;
+}
+
+moe_status_t moe_fp4_block_forward(const moe_fp4_weights_t* w, int32_t n_shared,
+                                   const uint16_t* router_w, const moe_block_norms_t* n,
+                                   const void* x, int32_t x_type, int32_t T, int32_t k, void* out,
+                                   void* workspace, size_t workspace_bytes, uint32_t flags,
+                                   hipStream_t stream) {
+  moe_status_t st = check_weights(w);
+  if (st != MOE_OK) return st;
+  st = check_full(T, k, w->E, w->H, n_shared);
+  if (st != MOE_OK) return st;
+  const int32_t E = w->E, H = w->H, I = w->I, ns = n_shared, Er = E - ns, kk = k + ns;
+  if (select_path((int64_t)T * kk, E, flags) < 0 || !n) return MOE_ERR_INVALID_ARGUMENT;
+  if (T == 0) return MOE_OK;
+  if (!router_w || !aligned(router_w, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  const BlockCarve c = block_carve(T, k, E, H, I, ns);
+  if (!workspace || workspace_bytes < c.total) return MOE_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint16_t* z = reinterpret_cast<uint16_t*>(ws + c.z);
+  float* y = reinterpret_cast<float*>(ws + c.y);
+  const FullCarve fc = full_carve(T, k, E, H, I, ns);
+  const LayerCarve& lc = fc.lc;
+  uint8_t* lw = ws + c.full + fc.layer;
+  // both norms' arguments are checked before anything is enqueued
+  st = check_norm_after(y, MOE_TYPE_FP32, x, x_type, n->w_post, nullptr, n->w_type, n->gate, n->gate_t,
+                        n->gate_h, n->eps, T, H, out, nullptr, nullptr, nullptr, MOE_QUANT_NONE);
+  if (st == MOE_OK)
+    st = check_norm_before(x, x_type, n->w_pre, n->w_type, T, H, n->eps, z, lw + lc.xq, lw + lc.xs,
+                           MOE_QUANT_MXFP8);
+  if (st != MOE_OK) return st;
+  // few tokens: the layer's fused front quantises z itself; otherwise the norm
+  // writes the experts' rows beside z (the same bytes, z is not read again)
+  const bool small = T <= kFrontMaxT;
+  st = moe_norm_before(x, x_type, n->w_pre, n->w_type, T, H, n->eps, z, small ? nullptr : lw + lc.xq,
+                       small ? nullptr : lw + lc.xs, small ? MOE_QUANT_NONE : MOE_QUANT_MXFP8, stream);
+  if (st != MOE_OK) return st;
+  float* rout = reinterpret_cast<float*>(ws + c.full + fc.rout);
+  const int S = router_slices(T, H, Er);
+  st = hip_status(launch_router_partials(z, router_w, T, H, Er, rout, rout, stream));
+  if (st != MOE_OK) return st;
+  int32_t* ids = reinterpret_cast<int32_t*>(lw + lc.ids);
+  float* gates = reinterpret_cast<float*>(lw + lc.gates);
+  int32_t* offsets = reinterpret_cast<int32_t*>(lw + lc.offsets);
+  int32_t* sorted = reinterpret_cast<int32_t*>(lw + lc.sorted);
+  int32_t* pos = reinterpret_cast<int32_t*>(lw + lc.pos);
+  if (small) {
+    st = run_front(rout, S, z, T, H, Er, k, ns, lw, lc, stream);
+  } else {
+    st = hip_status(launch_route_topk(rout, S, T, Er, k, ns, ids, gates, stream));
+    if (st == MOE_OK)
+      st = hip_status(launch_sort_permute(ids, T, E, kk, reinterpret_cast<int32_t*>(lw + lc.counts),
+                                          offsets, sorted, pos, lw + lc.sort_ws, stream));
+  }
+  if (st == MOE_OK)
+    st = moe_fp4_grouped_forward(w, lw + lc.xq, lw + lc.xs, gates, offsets, sorted, pos, T, kk, y,
+                                 lw + lc.fwd, lc.fwd_bytes, flags, stream);
+  if (st != MOE_OK) return st;
+  return moe_norm_after(y, MOE_TYPE_FP32, x, x_type, n->w_post, nullptr, n->w_type, n->gate, n->gate_t,
+                        n->gate_h, n->alpha, n->beta, n->eps, T, H, out, nullptr, nullptr, nullptr,
+                        MOE_QUANT_NONE, stream);
 }
 
 }  // extern "C"
