@@ -38,6 +38,10 @@ moe_status_t check_mx4_weights(const moe_mxfp4_weights_t* w) {
   return MOE_OK;
 }
 
+// The tiled product addresses activation rows by 32-bit byte offsets, up to
+// 4 KiB of which the instructions' own offsets take.
+bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K / 2 > ((int64_t)1 << 32) - 4096; }
+
 // 0: stream the weights, 1: tiled, -1: bad flags.  By default the weights are
 // streamed while the groups average at most `limit` rows.
 int choose_path(int64_t P, int E, uint32_t flags, int64_t limit) {
@@ -146,8 +150,7 @@ moe_status_t moe_mxfp4_dense_forward(const moe_mxfp4_weights_t* w, const uint8_t
   if (w->E != 1 || T < 0 || !norm_type(y_type)) return MOE_ERR_INVALID_ARGUMENT;
   const int path = choose_path(T, 1, flags, kStreamRows);
   if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
-  // activation rows are addressed by 32-bit byte offsets
-  if ((int64_t)T * w->K / 2 >= ((int64_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+  if (rows_too_large(T, w->K)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!xq || !xs || !y || !aligned(xq, 16) || !aligned(xs, 4) || !aligned(y, 16)) return MOE_ERR_INVALID_ARGUMENT;
   const Mx4Layout L(1, w->N, w->K, w->glu != 0);
@@ -169,7 +172,7 @@ moe_status_t moe_mxfp4_grouped_forward(const moe_mxfp4_weights_t* w, const uint8
   if (P < 0 || X < 0 || row_div < 1 || !norm_type(y_type)) return MOE_ERR_INVALID_ARGUMENT;
   const int path = choose_path(P, w->E, flags, kStreamRows);
   if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
-  if ((int64_t)X * w->K / 2 >= ((int64_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+  if (rows_too_large(X, w->K)) return MOE_ERR_UNSUPPORTED;
   if (P == 0) return MOE_OK;
   if (X < 1 || (!rows && X < P)) return MOE_ERR_INVALID_ARGUMENT;
   if (!xq || !xs || !offsets || !y) return MOE_ERR_INVALID_ARGUMENT;

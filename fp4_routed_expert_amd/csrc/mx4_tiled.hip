@@ -39,7 +39,6 @@ constexpr int kSA = kBM * 4;            // four scale bytes per row
 constexpr int kSW = kBT * 128;          // 64 lanes x 2 bytes per tile
 constexpr int kStage = kA + kW + kSA + kSW;
 constexpr int kSlots = 4;
-constexpr int kLoads = 10;              // DMA loads per wave and step
 constexpr int kIdx = kSlots * kStage;   // LDS offset of the next item's row indices
 constexpr int kLds = kIdx + kBM * 4;
 static_assert(kStage % 1024 == 0 && kLds <= 160 * 1024, "LDS");
@@ -128,20 +127,15 @@ __device__ __forceinline__ int lds_i32(uint32_t addr) {
   return *reinterpret_cast<const __attribute__((address_space(3))) int*>((uintptr_t)addr);
 }
 
-// The accumulating MFMA with its accumulator tied to AGPRs (left to itself the
-// compiler renames accumulators and copies them).  Volatile and ordered with
-// memory, so that every LDS read and DMA stays where the step places it.
-// The operands are read at issue; an accumulator's two MFMAs of a step are at
-// least four MFMAs apart.
+// One MFMA, its accumulator pinned to AGPRs at this point of the program and
+// the scheduler fenced, so that every LDS read and DMA stays where the step
+// places it.  (The builtin, not asm: the wait states between a vector write
+// and an MFMA that reads it are the compiler's then.)
 template <int kByte>
 __device__ __forceinline__ void mfma(v16f& c, const v4u& a, const v4u& b, uint32_t sa, uint32_t sb) {
-  if constexpr (kByte == 0)
-    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-                 : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb) : "memory");
-  else
-    asm volatile(
-        "v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-        : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb) : "memory");
+  c = mfma_fp4<kByte>(a, b, c, sa, sb);
+  asm volatile("" : "+a"(c) : : "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Where the DMA stands: the next step to load of the item it is in.
@@ -168,6 +162,55 @@ struct Ctx {
   int lane, wave;
 };
 
+// LDS-DMA blocks: the LDS address goes to M0 (restored after), the instruction
+// offset counts on both sides.  The base is copied by the scalar unit first: a
+// scalar register that a vector instruction has written (v_readfirstlane) must
+// not be read by a load within five wait states, and the compiler does not look
+// into the asm; the copy is also the wait state that M0 needs.
+__device__ __forceinline__ void dma_rows(const uint8_t* base, const uint32_t (&off)[4], uint32_t lds) {
+  const uint8_t* t;
+  uint32_t m;
+  asm volatile(
+      "s_mov_b32 %1, m0\n\t"
+      "s_mov_b32 m0, %7\n\t"
+      "s_mov_b64 %0, %6\n\t"
+      "global_load_lds_dwordx4 %2, %0\n\t"
+      "global_load_lds_dwordx4 %3, %0 offset:1024\n\t"
+      "global_load_lds_dwordx4 %4, %0 offset:2048\n\t"
+      "global_load_lds_dwordx4 %5, %0 offset:3072\n\t"
+      "s_mov_b32 m0, %1"
+      : "=&s"(t), "=&s"(m)
+      : "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base), "s"(lds)
+      : "memory");
+}
+__device__ __forceinline__ void dma_tile(const uint8_t* base, uint32_t off, uint32_t lds) {
+  const uint8_t* t;
+  uint32_t m;
+  asm volatile(
+      "s_mov_b32 %1, m0\n\t"
+      "s_mov_b32 m0, %4\n\t"
+      "s_mov_b64 %0, %3\n\t"
+      "global_load_lds_dwordx4 %2, %0\n\t"
+      "global_load_lds_dwordx4 %2, %0 offset:1024\n\t"
+      "s_mov_b32 m0, %1"
+      : "=&s"(t), "=&s"(m)
+      : "v"(off), "s"(base), "s"(lds)
+      : "memory");
+}
+__device__ __forceinline__ void dma_dwords(const uint8_t* base, uint32_t off, uint32_t lds) {
+  const uint8_t* t;
+  uint32_t m;
+  asm volatile(
+      "s_mov_b32 %1, m0\n\t"
+      "s_mov_b32 m0, %4\n\t"
+      "s_mov_b64 %0, %3\n\t"
+      "global_load_lds_dword %2, %0\n\t"
+      "s_mov_b32 m0, %1"
+      : "=&s"(t), "=&s"(m)
+      : "v"(off), "s"(base), "s"(lds)
+      : "memory");
+}
+
 // Row index DMA of item p (if there is one) into the index buffer; each wave
 // loads and later reads the 64 rows whose pieces it moves.
 __device__ __forceinline__ void fetch_rows(const Ctx& c, int p) {
@@ -176,8 +219,8 @@ __device__ __forceinline__ void fetch_rows(const Ctx& c, int p) {
   walk_item(c.walk, p, tt, tn);
   const Tile t = get_tile(c.a, c.ws, tt, c.walk.ntt);
   const uint32_t local = (uint32_t)min(64 * c.wave + c.lane, t.n - 1);
-  dma_x1(wave_ptr(reinterpret_cast<const uint8_t*>(c.a.rows + t.row0)), 4u * local,
-         wave_u32(c.lds + kIdx + 256u * (uint32_t)c.wave));
+  dma_dwords(wave_ptr(reinterpret_cast<const uint8_t*>(c.a.rows + t.row0)), 4u * local,
+             wave_u32(c.lds + kIdx + 256u * (uint32_t)c.wave));
 }
 
 // Points the cursor at item p (whose row indices are in the index buffer).
@@ -197,7 +240,7 @@ __device__ __forceinline__ void enter(const Ctx& c, Cursor& k, int p) {
     if (c.a.rows) x = (int)((uint32_t)lds_i32(c.lds + kIdx + 4 * r) / (uint32_t)c.a.div);
     x = max(min(x, c.a.X - 1), 0);
     if (u < 4)
-      k.a[u] = (uint32_t)x * rowb + piece;
+      k.a[u] = (uint32_t)x * rowb + piece + 3072u - 1024u * (uint32_t)u;
     else
       k.sa = (uint32_t)x * K32;
   }
@@ -209,19 +252,21 @@ __device__ __forceinline__ void enter(const Ctx& c, Cursor& k, int p) {
   k.j = 0;
 }
 
-// Load u (< 10) of the wave's share of the cursor's step into the slot at S:
-// 0-3 row pieces, 4-7 weight tiles, 8 row scales, 9 weight scales.
-__device__ __forceinline__ void issue1(const Ctx& c, const Cursor& k, uint32_t S, int u) {
-  if (u < 4)
-    dma_x4(wave_ptr(c.a.xq + (size_t)k.j * 64), k.a[u], S + 1024u * (uint32_t)(4 * c.wave + u));
-  else if (u < 8)
-    dma_x4(wave_ptr((u < 6 ? k.w0 : k.w1) + (size_t)k.j * 2048 + 1024 * (u & 1)), 16u * (uint32_t)c.lane,
-           S + (uint32_t)kA + 4096u * (uint32_t)c.wave + 1024u * (uint32_t)(u - 4));
-  else if (u == 8)
-    dma_x1(wave_ptr(c.a.xs + (size_t)k.j * 4), k.sa, S + (uint32_t)(kA + kW) + 256u * (uint32_t)c.wave);
-  else
-    dma_x1(wave_ptr(k.sw + (size_t)k.j * 256), 4u * (uint32_t)c.lane,
-           S + (uint32_t)(kA + kW + kSA) + 256u * (uint32_t)c.wave);
+// Block u (< 4) of the wave's share of the cursor's step into the slot at S:
+// its row pieces (4 loads), its weight tiles (2 and 2), both scales.
+constexpr int kBlocks = 4;
+__device__ __forceinline__ void issue1(const Ctx& c, const Cursor& k, uint32_t S, int j, int u) {
+  if (u == 0) {
+    // the rows' offsets have 1024 u taken off (and 3072 put on)
+    dma_rows(wave_ptr(c.a.xq + (size_t)j * 64 - 3072), k.a, S + 4096u * (uint32_t)c.wave);
+  } else if (u < 3) {
+    dma_tile(wave_ptr((u == 1 ? k.w0 : k.w1) + (size_t)j * 2048), 16u * (uint32_t)c.lane,
+             S + (uint32_t)kA + 4096u * (uint32_t)c.wave + 2048u * (uint32_t)(u - 1));
+  } else {
+    dma_dwords(wave_ptr(c.a.xs + (size_t)j * 4), k.sa, S + (uint32_t)(kA + kW) + 256u * (uint32_t)c.wave);
+    dma_dwords(wave_ptr(k.sw + (size_t)j * 256), 4u * (uint32_t)c.lane,
+               S + (uint32_t)(kA + kW + kSA) + 256u * (uint32_t)c.wave);
+  }
 }
 
 // After a step's loads: the next step, or the next item's first (past the
@@ -260,7 +305,6 @@ __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, in
   if constexpr (S > 0) {
     // first half: K-half 1's fragments arrive under K-half 0's MFMAs
     const uint32_t xa = cur + ad.a1, wa = cur + ad.w + 1024;
-    asm volatile("s_nop 1" ::: "memory");  // scales moved just before to the first MFMA that reads them
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       mfma<0>(acc[m >> 2][m & 3], f0.x[m >> 2], f0.w[m & 3], sx[m >> 2], sw[m & 3]);
@@ -275,6 +319,7 @@ __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, in
     }
   }
   uint32_t nsx[4], nsw[4];
+  const int kj = __builtin_amdgcn_readfirstlane(k.j);
   const uint32_t xa = nxt + ad.a0, wa = nxt + ad.w, sxa = nxt + ad.sa, swa = nxt + ad.sw;
   // what follows the barrier: the next step's K-half 0 and this slot's refill
   constexpr int kFirst = 2;                                // MFMAs in the pipe across the barrier
@@ -294,8 +339,8 @@ __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, in
         }
       }
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-      if (u * kLeft / kLoads == m) issue1(c, k, cur, u);
+    for (int u = 0; u < kBlocks; ++u)
+      if (u * kLeft / kBlocks == m) issue1(c, k, cur, kj, u);
   };
   auto publish = [&] {
     // this wave's loads of the next step have landed (20 newer ones may be in
@@ -370,9 +415,7 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
       for (int q = 0; q < 4; ++q) {
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][q][v] = 0.0f;
-        asm volatile("" : "+a"(acc[i][q]));
       }
-    asm volatile("s_nop 7" ::: "memory");  // accumulator writes before the first MFMA reads them
     const uint32_t s = c.lds + (uint32_t)(slot * kStage);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -390,12 +433,6 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
     slot = (slot + 1) & 3;
   }
   if constexpr (S > 0) {
-    // past the last MFMA's write before the accumulators are read
-    asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) asm volatile("" : "+a"(acc[i][q]));
     const int n = c.lane & 31, g = c.lane >> 5;
     constexpr int kO = kGlu ? 2 : 4;
     const int left = c.L.N / 32 - kO * group, f = left < kO ? left : kO;
@@ -407,6 +444,7 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
           const int m = 32 * (sub0 + i) + 8 * (v >> 2) + 4 * g + (v & 3);
           const float o[4] = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
           if (m < t.n) store_row<kGlu, kF32>(c, o, (size_t)t.row0 + m, group, f, n);
+          __builtin_amdgcn_sched_barrier(0);  // one row at a time out of the accumulators
         }
     }
   }
@@ -438,7 +476,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   for (int s = 0; s < kSlots; ++s) {
     const uint32_t S = wave_u32(c.lds + (uint32_t)(s * kStage));
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) issue1(c, k, S, u);
+    for (int u = 0; u < kBlocks; ++u) issue1(c, k, S, __builtin_amdgcn_readfirstlane(k.j), u);
     advance(c, k);
   }
   asm volatile("s_waitcnt vmcnt(30)\n\ts_barrier" ::: "memory");  // step 0 is there

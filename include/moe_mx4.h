@@ -91,7 +91,7 @@ moe_status_t moe_mxfp4_prepack(const uint8_t* wq, const uint8_t* ws, const uint8
  * operands MXFP4, accumulated in fp32 in the matrix cores and rounded once to
  * y_type (bf16, or fp32 as it is).
  *   xq [T, K/2] (16-byte aligned), xs [T, K/32] (4-byte aligned)
- *   y [T, N] (16-byte aligned); T * K < 2^33
+ *   y [T, N] (16-byte aligned); T * K <= 2^33 - 8192
  *   flags: MOE_FLAG_FORCE_DECODE streams the weights for every 32 tokens,
  *   MOE_FLAG_FORCE_PREFILL takes the tiled product; both compute the same
  *   function, by default the sizes decide.
@@ -113,7 +113,7 @@ moe_status_t moe_mxfp4_dense_forward(const moe_mxfp4_weights_t* w /*(host), E ==
  *   y [P, N] of y_type (16-byte aligned), rows in expert order
  *   workspace >= moe_mxfp4_grouped_workspace_size(P, E, N, K, glu) bytes,
  *     256-byte aligned; contents ignored on entry
- *   flags as above; X * K < 2^33
+ *   flags as above; X * K <= 2^33 - 8192
  */
 size_t moe_mxfp4_grouped_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K, int32_t glu);
 moe_status_t moe_mxfp4_grouped_forward(const moe_mxfp4_weights_t* w /*(host)*/, const uint8_t* xq, const uint8_t* xs,
