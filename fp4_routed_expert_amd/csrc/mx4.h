@@ -21,7 +21,8 @@ enum class ElemType : int { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
 // elements of one scale), so that a lane's two blocks are neighbours: a token
 // row's 64 bytes of a step are read as two 16-byte pieces at 32 g, and its
 // two scale bytes as one 16-bit word.  (Which K a lane holds is free as long
-// as both operands agree.)  A tile's K-steps are consecutive.
+// as both operands agree.)  A tile's K-steps are consecutive; an odd number of them is followed by one of
+// zeros.
 //
 // Columns: tiles come in groups of four, which one wave of the tiled kernel
 // multiplies.  The f tiles of a group (f = 4, fewer in the last) interleave
@@ -30,24 +31,23 @@ enum class ElemType : int { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
 // form the tiles alternate gate, up, gate, up; the two pairs of a group
 // interleave their 32 columns in the same way.
 //
-// Scales: per pair of tiles and K-step 256 bytes, [tile][lane][2]: lane's
-// bytes are the scales of its blocks of K-halves 0 and 1.  A last tile
-// without a partner leaves its partner's half unused.
+// Scales: per group of four tiles and pair of K-steps 1 KiB,
+// [lane][step][tile][2]: a lane's bytes are the scales of its blocks of K-halves
+// 0 and 1, so that one 128-bit read serves four tiles for two steps.  Tiles
+// that the last group lacks leave their bytes unused.
 struct Mx4Layout {
-  int E, N, K, J;  // J = K / 128 K-steps
-  int NT;          // 32-row tiles of an expert
+  int E, N, K, J, D;  // J = K / 128 K-steps, D pairs of them
+  int NT, NG;         // 32-row tiles of an expert, groups of four
   bool glu;
   size_t s_off, total;
   __host__ __device__ Mx4Layout(int E_, int N_, int K_, bool glu_)
-      : E(E_), N(N_), K(K_), J(K_ / 128), NT(N_ / 32 * (glu_ ? 2 : 1)), glu(glu_) {
-    s_off = (size_t)E * NT * J * 2048;
-    total = PackedLayout::align256(s_off + (size_t)E * ((NT + 1) / 2) * J * 256);
+      : E(E_), N(N_), K(K_), J(K_ / 128), D((J + 1) / 2), NT(N_ / 32 * (glu_ ? 2 : 1)), NG((NT + 3) / 4), glu(glu_) {
+    s_off = (size_t)E * NT * D * 4096;
+    total = PackedLayout::align256(s_off + (size_t)E * NG * D * 1024);
   }
-  __host__ __device__ size_t tile_off(int e, int nt) const { return ((size_t)e * NT + nt) * J * 2048; }
-  // scales of tile pair tp; K-step j is 256 j further, the pair's second tile 128
-  __host__ __device__ size_t scale_off(int e, int tp) const {
-    return s_off + ((size_t)e * ((NT + 1) / 2) + tp) * J * 256;
-  }
+  __host__ __device__ size_t tile_off(int e, int nt) const { return ((size_t)e * NT + nt) * D * 4096; }
+  // scales of group q; the next pair of K-steps is 1024 further
+  __host__ __device__ size_t scale_off(int e, int q) const { return s_off + ((size_t)e * NG + q) * D * 1024; }
   // output column of row n of tile nt
   __host__ __device__ int column(int nt, int n) const {
     if (glu) {
@@ -62,13 +62,13 @@ struct Mx4Layout {
 // One MFMA of 32 token rows x 32 weight rows x 64 K, both operands e2m1 (A:
 // lane l = 32 g + r holds token r's K block g; B likewise; D: lane l's element
 // v is token 8 (v / 4) + 4 (l / 32) + v % 4 of weight row l % 32), each lane's
-// scale byte kByte of sa / sb.
-template <int kByte>
+// scale byte kA of sa and kB of sb.
+template <int kA, int kB>
 __device__ __forceinline__ v16f mfma_fp4(v4u a, v4u b, v16f c, uint32_t sa, uint32_t sb) {
   const v4i ai = __builtin_bit_cast(v4i, a), bi = __builtin_bit_cast(v4i, b);
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
       __builtin_shufflevector(ai, ai, 0, 1, 2, 3, -1, -1, -1, -1),
-      __builtin_shufflevector(bi, bi, 0, 1, 2, 3, -1, -1, -1, -1), c, 4, 4, kByte, (int)sa, kByte, (int)sb);
+      __builtin_shufflevector(bi, bi, 0, 1, 2, 3, -1, -1, -1, -1), c, 4, 4, kA, (int)sa, kB, (int)sb);
 }
 
 // ------------------------------------------------------------------- MXFP4

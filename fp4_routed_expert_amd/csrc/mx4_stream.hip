@@ -23,21 +23,25 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint8_t* __restrict__ w
                                                    const uint8_t* __restrict__ uq, const uint8_t* __restrict__ us,
                                                    Mx4Layout L, uint8_t* __restrict__ packed) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  const size_t n = (size_t)L.E * L.NT * L.J * 128;
+  const size_t n = (size_t)L.E * L.NT * L.D * 256;
   if (i >= n) return;
   const int lane = (int)(i & 63), s = (int)(i >> 6) & 1;
   size_t t = i >> 7;
-  const int j = (int)(t % L.J);
-  t /= L.J;
+  const int j = (int)(t % (2 * L.D));
+  t /= 2 * L.D;
   const int nt = (int)(t % L.NT), e = (int)(t / L.NT);
   const int g = lane >> 5, col = L.column(nt, lane & 31);
   const bool up = L.glu && (nt & 1);
   const size_t row = (size_t)e * L.N + col;
   const int blk = 4 * j + 2 * g + s;
-  *reinterpret_cast<uint4*>(packed + L.tile_off(e, nt) + (size_t)j * 2048 + 1024 * s + 16 * lane) =
-      *reinterpret_cast<const uint4*>((up ? uq : wq) + row * (L.K / 2) + 16 * (size_t)blk);
-  packed[L.scale_off(e, nt >> 1) + (size_t)j * 256 + 128 * (nt & 1) + 2 * lane + s] =
-      (up ? us : ws)[row * (L.K / 32) + blk];
+  uint4 codes = make_uint4(0, 0, 0, 0);
+  uint8_t scale = 0;
+  if (j < L.J) {
+    codes = *reinterpret_cast<const uint4*>((up ? uq : wq) + row * (L.K / 2) + 16 * (size_t)blk);
+    scale = (up ? us : ws)[row * (L.K / 32) + blk];
+  }
+  *reinterpret_cast<uint4*>(packed + L.tile_off(e, nt) + (size_t)j * 2048 + 1024 * s + 16 * lane) = codes;
+  packed[L.scale_off(e, nt >> 2) + (size_t)(j >> 1) * 1024 + 16 * lane + 8 * (j & 1) + 2 * (nt & 3) + s] = scale;
 }
 
 // -------------------------------------------------------------------- stream
@@ -46,12 +50,12 @@ constexpr int kRows = 32;  // token rows of one pass
 template <int NT>
 struct Step {
   v4u w[NT][2], x[2];
-  uint32_t sw[NT], sx;
+  uint32_t sw, sx;
 };
 
-// wt[t] / st[t]: this lane's bytes of tile t and of its scales at K-step 0
+// wt[t] / st: this lane's bytes of tile t and of both tiles' scales at K-step 0
 template <int NT>
-__device__ __forceinline__ void load_step(Step<NT>& p, const uint8_t* const (&wt)[NT], const uint8_t* const (&st)[NT],
+__device__ __forceinline__ void load_step(Step<NT>& p, const uint8_t* const (&wt)[NT], const uint8_t* st,
                                           const uint8_t* xrow, const uint8_t* xscale, int j) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -59,20 +63,18 @@ __device__ __forceinline__ void load_step(Step<NT>& p, const uint8_t* const (&wt
     const uint8_t* w = wt[t] + (size_t)j * 2048;
     p.w[t][0] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(w));
     p.w[t][1] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(w + 1024));
-    p.sw[t] = *reinterpret_cast<const uint16_t*>(st[t] + (size_t)j * 256);
   }
+  p.sw = *reinterpret_cast<const uint32_t*>(st + (size_t)(j >> 1) * 1024 + 8 * (j & 1));
   p.x[0] = *reinterpret_cast<const v4u*>(xrow + (size_t)j * 64);
   p.x[1] = *reinterpret_cast<const v4u*>(xrow + (size_t)j * 64 + 16);
   p.sx = *reinterpret_cast<const uint16_t*>(xscale + (size_t)j * 4);
 }
 
-template <int NT>
-__device__ __forceinline__ void multiply(const Step<NT>& p, v16f (&acc)[NT]) {
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    acc[t] = mfma_fp4<0>(p.x[0], p.w[t][0], acc[t], p.sx, p.sw[t]);
-    acc[t] = mfma_fp4<1>(p.x[1], p.w[t][1], acc[t], p.sx, p.sw[t]);
-  }
+__device__ __forceinline__ void multiply(const Step<2>& p, v16f (&acc)[2]) {
+  acc[0] = mfma_fp4<0, 0>(p.x[0], p.w[0][0], acc[0], p.sx, p.sw);
+  acc[1] = mfma_fp4<0, 2>(p.x[0], p.w[1][0], acc[1], p.sx, p.sw);
+  acc[0] = mfma_fp4<1, 1>(p.x[1], p.w[0][1], acc[0], p.sx, p.sw);
+  acc[1] = mfma_fp4<1, 3>(p.x[1], p.w[1][1], acc[1], p.sx, p.sw);
 }
 
 template <int NW, int kB, bool kGlu, bool kF32>
@@ -97,13 +99,10 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(Mx4Args a, Mx4Layout L)
     stride = kRows * gridDim.y;
   }
   const uint8_t* wt[NT];
-  const uint8_t* st[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int nt = min(nt0 + t, L.NT - 1);  // a last tile without a partner is read twice, stored once
-    wt[t] = a.packed + L.tile_off(e, nt) + 16 * lane;
-    st[t] = a.packed + L.scale_off(e, nt >> 1) + 128 * (nt & 1) + 2 * lane;
-  }
+  for (int t = 0; t < NT; ++t)  // a last tile without a partner is read twice, stored once
+    wt[t] = a.packed + L.tile_off(e, min(nt0 + t, L.NT - 1)) + 16 * lane;
+  const uint8_t* st = a.packed + L.scale_off(e, nt0 >> 2) + 16 * lane + 2 * (nt0 & 3);
   const int nsteps = J > wave ? (J - wave + NW - 1) / NW : 0;
   for (int m0 = begin; m0 < end; m0 += stride) {
     const int rows = min(kRows, end - m0);
@@ -124,11 +123,11 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(Mx4Args a, Mx4Layout L)
 #pragma unroll
       for (int b = 0; b < kB; ++b) load_step<NT>(p[b], wt, st, xrow, xscale, wave + NW * (u + b));
 #pragma unroll
-      for (int b = 0; b < kB; ++b) multiply<NT>(p[b], acc);
+      for (int b = 0; b < kB; ++b) multiply(p[b], acc);
     }
     for (; u < nsteps; ++u) {
       load_step<NT>(p[0], wt, st, xrow, xscale, wave + NW * u);
-      multiply<NT>(p[0], acc);
+      multiply(p[0], acc);
     }
     // element v of a lane is token 8 (v / 4) + 4 g + v % 4: only the groups of
     // eight tokens that exist are joined
@@ -189,7 +188,7 @@ void stream_as(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, hipStream_t 
 
 hipError_t launch_mx4_pack(const uint8_t* wq, const uint8_t* ws, const uint8_t* uq, const uint8_t* us,
                            const Mx4Layout& L, uint8_t* packed, hipStream_t st) {
-  const size_t n = (size_t)L.E * L.NT * L.J * 128;
+  const size_t n = (size_t)L.E * L.NT * L.D * 256;
   hipLaunchKernelGGL(pack_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, wq, ws, uq, us, L, packed);
   return hipGetLastError();
 }

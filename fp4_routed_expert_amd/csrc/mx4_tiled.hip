@@ -3,26 +3,31 @@
 // where an expert's rows are few.
 //
 // A work item is 256 rows of one group x 8 weight tiles (256 weight rows).
-// Four waves, one per SIMD, in a 2 x 2 grid, each with up to four 32-token
-// sub-tiles x four weight tiles: 16 accumulators of 32 x 32 (256 registers).
-// v_mfma_scale_f32_32x32x64_f8f6f4 rather than 16x16x128: with one wave per
-// SIMD the larger instruction issues at 6.2-6.6 PFLOP/s on random operands,
-// the smaller one at 4.4-5.1 (it lasts 16 clocks, too few to issue anything
-// else under), and it reads half as many operand registers per flop.
+// Eight waves, two per SIMD, in a 4 x 2 grid, each with up to two 32-token
+// sub-tiles x four weight tiles: 8 accumulators of 32 x 32 (128 registers).
+// v_mfma_scale_f32_32x32x64_f8f6f4 rather than 16x16x128: it lasts 32 clocks
+// instead of 16, so that the other instructions find room beside it, and reads
+// half as many operand registers per flop (back to back on random operands:
+// 6.2-6.6 PFLOP/s, where the power limit holds the clock; the smaller one
+// 4.4-5.1 with one wave per SIMD, 6.5 with two).
 //
-// K runs in steps of 128.  A step's 34 KiB (row pieces, weight tiles, both
-// sides' scales) go from global memory to LDS by LDS-DMA into a ring of four
-// slots, three steps ahead; one barrier per step, in its second half,
-// publishes the next step and frees the current one's slot, which is refilled
-// at once.  Fragments are read from LDS half a step before their use.  Row r's
-// four 16-byte pieces lie at piece p ^ (r / 4 % 4), which spreads the 16 rows
-// that one LDS cycle serves over all banks.
+// K runs in steps of 128, two to a stage: 32 KiB of row pieces (128 bytes of
+// each row: at 64 bytes a row the L2 requests alone take as long as the
+// MFMAs), four weight half-stages and the scales go from global memory to LDS
+// by LDS-DMA into two stages.  One barrier per step, in its second half,
+// publishes what the next step reads and frees what the last one has read,
+// which is refilled at once with the data of two stages on: weights of a step
+// come three steps before their use, rows and scales two.  Every wave issues
+// the same ten loads per stage in the same order, dummy stages past the end, so
+// that fixed wait counts serve every stage.  Fragments are read from LDS half a
+// step before their use.  Row r's eight 16-byte pieces lie at piece
+// p ^ (r / 2 % 8), which spreads the 16 rows that one LDS cycle serves over all
+// banks.
 //
 // The workgroups are persistent: one per CU (its LDS allows no second) walks
-// its XCD's contiguous share of the items, and the ring runs on across items,
-// so that an item's first steps arrive under the last steps and the stores of
-// the one before.  Every wave issues the same ten loads per step, dummy steps
-// past the end, so one fixed wait count serves all steps.
+// its XCD's contiguous share of the items, and the stages run on across items,
+// so that an item's first stages arrive under the last steps and the stores of
+// the one before.
 #include <atomic>
 
 #include "lds_dma.h"
@@ -33,14 +38,15 @@ namespace {
 
 constexpr int kBM = 256;                // rows of an item
 constexpr int kBT = 8;                  // weight tiles of an item
-constexpr int kA = kBM * 64;            // row pieces of a step
-constexpr int kW = kBT * 2048;          // weight tiles
-constexpr int kSA = kBM * 4;            // four scale bytes per row
-constexpr int kSW = kBT * 128;          // 64 lanes x 2 bytes per tile
-constexpr int kStage = kA + kW + kSA + kSW;
-constexpr int kSlots = 4;
-constexpr int kIdx = kSlots * kStage;   // LDS offset of the next item's row indices
-constexpr int kLds = kIdx + kBM * 4;
+constexpr int kWaves = 8;
+constexpr int kA = kBM * 128;           // row pieces of a stage
+constexpr int kW = kBT * 2048;          // weight tiles of a step
+constexpr int kSA = kBM * 8;            // eight scale bytes per row
+constexpr int kSW = 2 * 1024;           // weight scales of two groups of four tiles
+constexpr int kOffW = kA, kOffSA = kA + 2 * kW, kOffSW = kOffSA + kSA;
+constexpr int kStage = kA + 2 * kW + kSA + kSW;
+constexpr int kIdx = 2 * kStage;        // LDS offset of the next item's row indices
+constexpr int kLds = kIdx + kWaves * 256 + kBM * 8;
 static_assert(kStage % 1024 == 0 && kLds <= 160 * 1024, "LDS");
 
 // One entry per 256 rows (at most) of a group, of equal heights.
@@ -120,9 +126,6 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 __device__ __forceinline__ v4u lds_v4(uint32_t addr) {
   return *reinterpret_cast<const __attribute__((address_space(3))) v4u*>((uintptr_t)addr);
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>((uintptr_t)addr);
-}
 __device__ __forceinline__ int lds_i32(uint32_t addr) {
   return *reinterpret_cast<const __attribute__((address_space(3))) int*>((uintptr_t)addr);
 }
@@ -131,25 +134,27 @@ __device__ __forceinline__ int lds_i32(uint32_t addr) {
 // the scheduler fenced, so that every LDS read and DMA stays where the step
 // places it.  (The builtin, not asm: the wait states between a vector write
 // and an MFMA that reads it are the compiler's then.)
-template <int kByte>
+template <int kA, int kB>
 __device__ __forceinline__ void mfma(v16f& c, const v4u& a, const v4u& b, uint32_t sa, uint32_t sb) {
-  c = mfma_fp4<kByte>(a, b, c, sa, sb);
+  c = mfma_fp4<kA, kB>(a, b, c, sa, sb);
   asm volatile("" : "+a"(c) : : "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Where the DMA stands: the next step to load of the item it is in.
+// Where the DMA stands: the next stage to load of the item it is in.  The
+// pointers (uniform) are that stage's.
 struct Cursor {
-  const uint8_t* w0;  // the wave's two weight tiles at K-step 0
-  const uint8_t* w1;
-  const uint8_t* sw;  // and their pair's scales
-  uint32_t a[4];      // per lane: byte offset of its piece of rows 64 w + 16 u + l / 4
-  uint32_t sa;        // of row 64 w + l's scales
-  int p, j;           // item, step
+  const uint8_t* x;   // activation codes
+  const uint8_t* w;   // the wave's weight tile
+  const uint8_t* xs;  // activation scales
+  const uint8_t* ws;  // the wave's part of the weight scales
+  uint32_t a[4];      // per lane: its piece of rows 32 w + 8 u + l / 8
+  uint32_t sa;        // per lane: its dword of row scales
+  int p, left;        // item, stages left of it (this one counted)
 };
 
 struct Frag {
-  v4u x[4], w[4];
+  v4u x[2], w[4];
 };
 
 struct Ctx {
@@ -162,65 +167,80 @@ struct Ctx {
   int lane, wave;
 };
 
-// LDS-DMA blocks: the LDS address goes to M0 (restored after), the instruction
-// offset counts on both sides.  The base is copied by the scalar unit first: a
-// scalar register that a vector instruction has written (v_readfirstlane) must
-// not be read by a load within five wait states, and the compiler does not look
-// into the asm; the copy is also the wait state that M0 needs.
-__device__ __forceinline__ void dma_rows(const uint8_t* base, const uint32_t (&off)[4], uint32_t lds) {
+// LDS-DMA: lane l's 16 (4) bytes at base + off go to LDS address lds + 16 l
+// (4 l); an instruction offset counts on both sides.  The LDS address goes to
+// M0, which nothing else here uses (LDS instructions need none).  The base is
+// copied by the scalar unit first: a scalar register that a vector instruction
+// has written (v_readfirstlane) must not be read by a load within five wait
+// states, and the compiler does not look into the asm; the copy is also the
+// wait state that M0 needs.
+template <int kOff = 0>
+__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
   const uint8_t* t;
-  uint32_t m;
   asm volatile(
-      "s_mov_b32 %1, m0\n\t"
-      "s_mov_b32 m0, %7\n\t"
-      "s_mov_b64 %0, %6\n\t"
-      "global_load_lds_dwordx4 %2, %0\n\t"
-      "global_load_lds_dwordx4 %3, %0 offset:1024\n\t"
-      "global_load_lds_dwordx4 %4, %0 offset:2048\n\t"
-      "global_load_lds_dwordx4 %5, %0 offset:3072\n\t"
-      "s_mov_b32 m0, %1"
-      : "=&s"(t), "=&s"(m)
-      : "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base), "s"(lds)
+      "s_mov_b32 m0, %3\n\t"
+      "s_mov_b64 %0, %2\n\t"
+      "global_load_lds_dwordx4 %1, %0 offset:%4"
+      : "=&s"(t)
+      : "v"(off), "s"(base), "s"(lds), "n"(kOff)
       : "memory");
 }
-__device__ __forceinline__ void dma_tile(const uint8_t* base, uint32_t off, uint32_t lds) {
+__device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
   const uint8_t* t;
-  uint32_t m;
   asm volatile(
-      "s_mov_b32 %1, m0\n\t"
-      "s_mov_b32 m0, %4\n\t"
-      "s_mov_b64 %0, %3\n\t"
-      "global_load_lds_dwordx4 %2, %0\n\t"
-      "global_load_lds_dwordx4 %2, %0 offset:1024\n\t"
-      "s_mov_b32 m0, %1"
-      : "=&s"(t), "=&s"(m)
-      : "v"(off), "s"(base), "s"(lds)
-      : "memory");
-}
-__device__ __forceinline__ void dma_dwords(const uint8_t* base, uint32_t off, uint32_t lds) {
-  const uint8_t* t;
-  uint32_t m;
-  asm volatile(
-      "s_mov_b32 %1, m0\n\t"
-      "s_mov_b32 m0, %4\n\t"
-      "s_mov_b64 %0, %3\n\t"
-      "global_load_lds_dword %2, %0\n\t"
-      "s_mov_b32 m0, %1"
-      : "=&s"(t), "=&s"(m)
+      "s_mov_b32 m0, %3\n\t"
+      "s_mov_b64 %0, %2\n\t"
+      "global_load_lds_dword %1, %0"
+      : "=&s"(t)
       : "v"(off), "s"(base), "s"(lds)
       : "memory");
 }
 
-// Row index DMA of item p (if there is one) into the index buffer; each wave
-// loads and later reads the 64 rows whose pieces it moves.
+// Sub-tiles of 32 rows that wave row wm (of four) takes of a tile of n rows:
+// how many, and the first one.  Wave rows 0 and 2 share SIMDs, as do 1 and 3.
+__device__ __forceinline__ int sub_tiles(int n, int wm) { return ((n + 31) / 32 + 3 - wm) / 4; }
+__device__ __forceinline__ int first_sub(int n, int wm) {
+  const int n32 = (n + 31) / 32;
+  return wm * (n32 / 4) + min(wm, n32 % 4);
+}
+
+// Row of the tile whose scale dword (l % 2: which step's) lane l of wave w
+// moves: the scales of wave row wm's two sub-tiles lie side by side
+// ([row 32][sub-tile 2][8 bytes]), so that one 128-bit read serves both.
+__device__ __forceinline__ int scale_row(int n, int wave, int lane) {
+  const int at = 64 * (wave & 1) + lane;
+  return 32 * (first_sub(n, wave >> 1) + ((at >> 1) & 1)) + (at >> 2);
+}
+
+// Row index DMA of item p (if there is one) into the index buffer: each wave
+// loads, and later reads, the indices of the rows whose pieces (32 of them) and
+// of those whose scales it moves.
 __device__ __forceinline__ void fetch_rows(const Ctx& c, int p) {
   if (!c.a.rows || p >= c.walk.hi) return;
   int tt, tn;
   walk_item(c.walk, p, tt, tn);
   const Tile t = get_tile(c.a, c.ws, tt, c.walk.ntt);
-  const uint32_t local = (uint32_t)min(64 * c.wave + c.lane, t.n - 1);
-  dma_dwords(wave_ptr(reinterpret_cast<const uint8_t*>(c.a.rows + t.row0)), 4u * local,
-             wave_u32(c.lds + kIdx + 256u * (uint32_t)c.wave));
+  const uint8_t* base = wave_ptr(reinterpret_cast<const uint8_t*>(c.a.rows + t.row0));
+  const uint32_t at = wave_u32(c.lds + kIdx + 256u * (uint32_t)c.wave);
+  dma4(base, 4u * (uint32_t)min(32 * c.wave + (c.lane & 31), t.n - 1), at);
+  dma4(base, 4u * (uint32_t)min(scale_row(t.n, c.wave, c.lane), t.n - 1), at + 256u * kWaves);
+}
+
+// x row of row r of tile t; at: where the index buffer has its index.
+__device__ __forceinline__ uint32_t x_row(const Ctx& c, const Tile& t, int r, int at) {
+  int x = t.row0 + min(r, t.n - 1);  // rows past the tile read its last one
+  if (c.a.rows) x = (int)((uint32_t)lds_i32(c.lds + kIdx + 4 * at) / (uint32_t)c.a.div);
+  return (uint32_t)max(min(x, c.a.X - 1), 0);
+}
+
+// The last stage of an odd number of steps has no second step.  Its weights are
+// zeros; for the rows, what would lie past their end reads the first step's
+// bytes (a block that is NaN there is NaN in the first step too).
+__device__ __forceinline__ void clip_tail(const Ctx& c, Cursor& k) {
+  if (k.left != 1 || !(c.L.J & 1)) return;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) k.a[u] -= (((uint32_t)c.lane & 7) ^ (uint32_t)((c.lane >> 4) + 4 * (u & 1))) & 4 ? 64u : 0u;
+  k.sa -= 4u * (uint32_t)(c.lane & 1);
 }
 
 // Points the cursor at item p (whose row indices are in the index buffer).
@@ -229,140 +249,183 @@ __device__ __forceinline__ void enter(const Ctx& c, Cursor& k, int p) {
   walk_item(c.walk, p, tt, tn);
   const Tile t = get_tile(c.a, c.ws, tt, c.walk.ntt);
   const Mx4Layout& L = c.L;
-  const uint32_t rowb = (uint32_t)L.K / 2, K32 = (uint32_t)L.K / 32;
-  // logical piece of the lane: physical piece l % 4 of a row whose r / 4 % 4 is l / 16
-  const uint32_t piece = (uint32_t)(((c.lane & 3) ^ (c.lane >> 4)) << 4);
 #pragma unroll
-  for (int u = 0; u < 5; ++u) {
-    const int r = 64 * c.wave + (u < 4 ? 16 * u + (c.lane >> 2) : c.lane);
-    const int m = min(r, t.n - 1);  // rows past the tile read its last one
-    int x = t.row0 + m;
-    if (c.a.rows) x = (int)((uint32_t)lds_i32(c.lds + kIdx + 4 * r) / (uint32_t)c.a.div);
-    x = max(min(x, c.a.X - 1), 0);
-    if (u < 4)
-      k.a[u] = (uint32_t)x * rowb + piece + 3072u - 1024u * (uint32_t)u;
-    else
-      k.sa = (uint32_t)x * K32;
+  for (int u = 0; u < 4; ++u) {
+    const int r = 8 * u + (c.lane >> 3);
+    // logical piece of the lane: physical piece l % 8 of a row whose r / 2 % 8 is l / 16 + 4 (u % 2)
+    const uint32_t piece = ((uint32_t)c.lane & 7) ^ (uint32_t)((c.lane >> 4) + 4 * (u & 1));
+    k.a[u] = x_row(c, t, 32 * c.wave + r, 64 * c.wave + r) * ((uint32_t)L.K / 2) + 16u * piece;
   }
-  const int nt = tn * kBT + 2 * c.wave;
-  k.w0 = wave_ptr(c.a.packed + L.tile_off(t.e, min(nt, L.NT - 1)));
-  k.w1 = wave_ptr(c.a.packed + L.tile_off(t.e, min(nt + 1, L.NT - 1)));
-  k.sw = wave_ptr(c.a.packed + L.scale_off(t.e, min(nt, L.NT - 1) >> 1));
+  k.sa = x_row(c, t, scale_row(t.n, c.wave, c.lane), 64 * kWaves + 64 * c.wave + c.lane) * ((uint32_t)L.K / 32) +
+         4u * (uint32_t)(c.lane & 1);
+  k.x = wave_ptr(c.a.xq);
+  k.xs = wave_ptr(c.a.xs);
+  // tiles past the last one read the last one; their columns are not stored
+  k.w = wave_ptr(c.a.packed + L.tile_off(t.e, min(tn * kBT + c.wave, L.NT - 1)));
+  k.ws = wave_ptr(c.a.packed + L.scale_off(t.e, min(2 * tn + (c.wave >> 2), L.NG - 1)) + 256 * (c.wave & 3));
   k.p = p;
-  k.j = 0;
+  k.left = L.D;
+  clip_tail(c, k);
 }
 
-// Block u (< 4) of the wave's share of the cursor's step into the slot at S:
-// its row pieces (4 loads), its weight tiles (2 and 2), both scales.
-constexpr int kBlocks = 4;
-__device__ __forceinline__ void issue1(const Ctx& c, const Cursor& k, uint32_t S, int j, int u) {
-  if (u == 0) {
-    // the rows' offsets have 1024 u taken off (and 3072 put on)
-    dma_rows(wave_ptr(c.a.xq + (size_t)j * 64 - 3072), k.a, S + 4096u * (uint32_t)c.wave);
-  } else if (u < 3) {
-    dma_tile(wave_ptr((u == 1 ? k.w0 : k.w1) + (size_t)j * 2048), 16u * (uint32_t)c.lane,
-             S + (uint32_t)kA + 4096u * (uint32_t)c.wave + 2048u * (uint32_t)(u - 1));
-  } else {
-    dma_dwords(wave_ptr(c.a.xs + (size_t)j * 4), k.sa, S + (uint32_t)(kA + kW) + 256u * (uint32_t)c.wave);
-    dma_dwords(wave_ptr(k.sw + (size_t)j * 256), 4u * (uint32_t)c.lane,
-               S + (uint32_t)(kA + kW + kSA) + 256u * (uint32_t)c.wave);
+// Load u (< 10) of the wave's share of the cursor's stage into the one at S, in
+// the order of their use: 0-1 the first step's weights, 2-5 row pieces, 6-7
+// scales, 8-9 the second step's weights.
+__device__ __forceinline__ void issue(const Ctx& c, const Cursor& k, uint32_t S, int u) {
+  const uint32_t w = (uint32_t)c.wave, l16 = 16u * (uint32_t)c.lane;
+  switch (u) {
+    case 0: dma16(k.w, l16, S + (uint32_t)kOffW + 2048u * w); break;
+    case 1: dma16<1024>(k.w, l16, S + (uint32_t)kOffW + 2048u * w); break;
+    case 2: dma16(k.x, k.a[0], S + 4096u * w); break;
+    case 3: dma16(k.x, k.a[1], S + 4096u * w + 1024u); break;
+    case 4: dma16(k.x, k.a[2], S + 4096u * w + 2048u); break;
+    case 5: dma16(k.x, k.a[3], S + 4096u * w + 3072u); break;
+    case 6: dma4(k.xs, k.sa, S + (uint32_t)kOffSA + 256u * w); break;
+    case 7: dma4(k.ws, 4u * (uint32_t)c.lane, S + (uint32_t)kOffSW + 256u * w); break;
+    case 8: dma16(k.w + 2048, l16, S + (uint32_t)(kOffW + kW) + 2048u * w); break;
+    default: dma16<1024>(k.w + 2048, l16, S + (uint32_t)(kOffW + kW) + 2048u * w);
   }
 }
 
-// After a step's loads: the next step, or the next item's first (past the
-// last item its steps are loaded again and never used).
+// After a stage's loads: the next stage, or the next item's first (past the
+// last item its last stage is loaded again and never used).
 __device__ __forceinline__ void advance(const Ctx& c, Cursor& k) {
-  if (++k.j < c.L.J) return;
-  const int p = k.p + c.stride;
-  if (p >= c.walk.hi) {
-    k.j = 0;
+  if (k.left > 1) {
+    --k.left;
+    k.x += 128;
+    k.w += 4096;
+    k.xs += 8;
+    k.ws += 1024;
+    clip_tail(c, k);
     return;
   }
-  // the indices were loaded when the cursor entered this item; with more steps
-  // than the prologue's four the per-step waits have covered them
-  if (c.a.rows && c.L.J <= kSlots) wait_vmcnt<0>();
+  const int p = k.p + c.stride;
+  if (p >= c.walk.hi) return;
+  // the indices were loaded when the cursor entered this item; with three
+  // stages or more since then the waits of the steps have covered them
+  if (c.a.rows && c.L.D < 3) wait_vmcnt<0>();
   enter(c, k, p);
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the indices are read before they are replaced
   fetch_rows(c, p + c.stride);
 }
 
-struct Addr {  // per lane, relative to a slot
-  uint32_t a0, a1;  // row r of the wave's first sub-tile, pieces of K-halves 0 and 1 (sub-tile i at + 2048 i)
-  uint32_t sa;      // its scale pair (+ 128 i)
-  uint32_t w;       // weight tile 4 wn (+ 2048 t, K-half 1 at + 1024)
-  uint32_t sw;      // its scale pair (+ 128 t)
+struct Addr {  // per lane, relative to a stage
+  uint32_t a[4];   // row r of the wave's first sub-tile, pieces of the four K-halves (sub-tile i at + 4096 i)
+  uint32_t sa;     // its sub-tiles' scales
+  uint32_t w;      // first step's weight tile 4 wn (+ 2048 t, K-half 1 at + 1024, second step at + kW)
+  uint32_t sw;     // the group's scales
+  uint32_t shift;  // 16 g: the lane's half of a row's scale dword
 };
 
-// One K-step of a wave with S live sub-tiles.  On entry f0 and the scales hold
-// K-half 0's fragments of this step; on exit those of the next one.
+struct Scales {
+  uint32_t x[2][2];  // sub-tile, step
+  v4u w;             // two dwords per step
+};
+
+// Fragments q (< S + 4) of a K-half: four weight tiles, then S sub-tiles.
+__device__ __forceinline__ void read_frag(Frag& f, uint32_t xa, uint32_t wa, int q) {
+  if (q < 4)
+    f.w[q] = lds_v4(wa + 2048 * q);
+  else
+    f.x[q - 4] = lds_v4(xa + 4096 * (q - 4));
+}
+
 template <int S>
-__device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, int slot, v16f (&acc)[4][4], Frag& f0,
-                                     Frag& f1, uint32_t (&sx)[4], uint32_t (&sw)[4]) {
-  const uint32_t cur = wave_u32(c.lds + (uint32_t)(slot * kStage));
-  const uint32_t nxt = wave_u32(c.lds + (uint32_t)(((slot + 1) & 3) * kStage));
-  constexpr int M = 4 * S;       // MFMAs of a half
-  constexpr int R = S + 4;       // fragments of a half
+__device__ __forceinline__ void read_scales(Scales& s, uint32_t stage, const Addr& ad, v4u& raw) {
+  raw = lds_v4(stage + ad.sa);
+  s.w = lds_v4(stage + ad.sw);
+}
+template <int S>
+__device__ __forceinline__ void shift_scales(Scales& s, const Addr& ad, const v4u& raw) {
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    s.x[i][0] = raw[2 * i] >> ad.shift;
+    s.x[i][1] = raw[2 * i + 1] >> ad.shift;
+  }
+}
+
+// MFMA m of K-half kHalf of step H: sub-tile m / 4, tile m % 4 (whose scale is
+// byte 2 (m % 2) + kHalf of its pair's dword).
+template <int H, int kHalf>
+__device__ __forceinline__ void multiply(v16f (&acc)[2][4], const Frag& f, const Scales& s, int m) {
+  const int i = m >> 2, t = m & 3;
+  if (t & 1)
+    mfma<kHalf, 2 + kHalf>(acc[i][t], f.x[i], f.w[t], s.x[i][H], s.w[2 * H + (t >> 1)]);
+  else
+    mfma<kHalf, kHalf>(acc[i][t], f.x[i], f.w[t], s.x[i][H], s.w[2 * H + (t >> 1)]);
+}
+
+// Step H (0, 1) of the stage at `cur` for a wave with S live sub-tiles.  On
+// entry f0 holds K-half 0's fragments of this step and s the stage's scales;
+// on exit the same for the next step.  Loads: the cursor's stage goes to where
+// this one is; in step 0 its first step's weights (whose place is free behind
+// the barrier), in step 1 the row pieces and, in the next stage's step 0, the
+// rest, spread over the MFMAs.
+template <int S, int H>
+__device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, uint32_t cur, uint32_t nxt,
+                                     v16f (&acc)[2][4], Frag& f0, Frag& f1, Scales& s) {
+  constexpr int M = 4 * S;  // MFMAs of a half
+  constexpr int R = S + 4;  // fragments of a half
+  // first half: K-half 1's fragments arrive under K-half 0's MFMAs
   if constexpr (S > 0) {
-    // first half: K-half 1's fragments arrive under K-half 0's MFMAs
-    const uint32_t xa = cur + ad.a1, wa = cur + ad.w + 1024;
+    const uint32_t xa = cur + ad.a[2 * H + 1], wa = cur + ad.w + (uint32_t)(H * kW + 1024);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      mfma<0>(acc[m >> 2][m & 3], f0.x[m >> 2], f0.w[m & 3], sx[m >> 2], sw[m & 3]);
+      multiply<H, 0>(acc, f0, s, m);
 #pragma unroll
       for (int q = 0; q < R; ++q)
-        if (q * M / (2 * R) == m) {
-          if (q < 4)
-            f1.w[q] = lds_v4(wa + 2048 * q);
-          else
-            f1.x[q - 4] = lds_v4(xa + 2048 * (q - 4));
-        }
-    }
-  }
-  uint32_t nsx[4], nsw[4];
-  const int kj = __builtin_amdgcn_readfirstlane(k.j);
-  const uint32_t xa = nxt + ad.a0, wa = nxt + ad.w, sxa = nxt + ad.sa, swa = nxt + ad.sw;
-  // what follows the barrier: the next step's K-half 0 and this slot's refill
-  constexpr int kFirst = 2;                                // MFMAs in the pipe across the barrier
-  constexpr int kLeft = S > 0 ? M - kFirst : 1;            // MFMAs after it
-  auto after = [&](int m) {
-    // m-th of kLeft places: its share of the fragments (in the first half of
-    // the places) and of the ten loads
+        if (q * M / R == m) read_frag(f1, xa, wa, q);
+      if constexpr (H == 0) {
 #pragma unroll
-    for (int q = 0; q < R; ++q)
-      if (S > 0 && q * kLeft / (2 * R) == m) {
-        if (q < 4) {
-          f0.w[q] = lds_v4(wa + 2048 * q);
-          nsw[q] = lds_u16(swa + 128 * q);
-        } else {
-          f0.x[q - 4] = lds_v4(xa + 2048 * (q - 4));
-          nsx[q - 4] = lds_u16(sxa + 128 * (q - 4));
-        }
+        for (int u = 6; u < 10; ++u)
+          if ((u - 6) * M / 4 + M / 8 == m) issue(c, k, nxt, u);
       }
+    }
+  } else if constexpr (H == 0) {
 #pragma unroll
-    for (int u = 0; u < kBlocks; ++u)
-      if (u * kLeft / kBlocks == m) issue1(c, k, cur, kj, u);
-  };
+    for (int u = 6; u < 10; ++u) issue(c, k, nxt, u);
+  }
+  if constexpr (H == 0) advance(c, k);
   auto publish = [&] {
-    // this wave's loads of the next step have landed (20 newer ones may be in
-    // flight) and its reads of this step are done; then everyone's
-    asm volatile("s_waitcnt vmcnt(20) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    // This wave's loads of what the next step reads have landed and its reads
+    // of this step are done; then everyone's.  In flight may be, behind step 0,
+    // the next stage (10) and, behind step 1, the next stage's second weights
+    // and the first ones of the stage after it (4).
+    if constexpr (H == 0)
+      asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
+  constexpr int kFrom = H == 0 ? 0 : 2, kTo = H == 0 ? 2 : 6;  // this step's loads behind the barrier
   if constexpr (S > 0) {
+    constexpr int kLeft = M - 1;  // places behind the barrier, which stands after the first MFMA
+    const uint32_t xa = (H == 0 ? cur + ad.a[2] : nxt + ad.a[0]);
+    const uint32_t wa = (H == 0 ? cur + ad.w + (uint32_t)kW : nxt + ad.w);
+    v4u raw;
+    Scales ns;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      mfma<1>(acc[m >> 2][m & 3], f1.x[m >> 2], f1.w[m & 3], sx[m >> 2], sw[m & 3]);
-      if (m == kFirst - 1) publish();
-      if (m >= kFirst - 1 && m < M - 1) after(m - (kFirst - 1));
+      multiply<H, 1>(acc, f1, s, m);
+      if (m == 0) {
+        publish();
+        if constexpr (H == 1) read_scales<S>(ns, nxt, ad, raw);
+      }
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+        if (q * kLeft / R == m) read_frag(f0, xa, wa, q);
+#pragma unroll
+      for (int u = kFrom; u < kTo; ++u)
+        if ((u - kFrom) * kLeft / (kTo - kFrom) + kLeft / 8 == m) issue(c, k, cur, u);
     }
-#pragma unroll
-    for (int i = 0; i < S; ++i) sx[i] = nsx[i];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) sw[t] = nsw[t];
+    if constexpr (H == 1) {
+      shift_scales<S>(ns, ad, raw);
+      s = ns;
+    }
   } else {
     publish();
-    after(0);
+#pragma unroll
+    for (int u = kFrom; u < kTo; ++u) issue(c, k, cur, u);
   }
-  advance(c, k);
 }
 
 // Stores of a wave's S sub-tiles: element v of a lane is row 8 (v / 4) + 4 g +
@@ -403,34 +466,31 @@ __device__ __forceinline__ void store_row(const Ctx& c, const float (&v)[4], siz
 }
 
 template <int S, bool kGlu, bool kF32>
-__device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad, int& slot, const Tile& t, int sub0,
+__device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad, int& stage, const Tile& t, int sub0,
                                          int group) {
-  v16f acc[4][4];
+  v16f acc[2][4];
   Frag f0, f1;
-  uint32_t sx[4], sw[4];
+  Scales s;
+  uint32_t cur = wave_u32(c.lds + (uint32_t)(stage * kStage)), nxt;
   if constexpr (S > 0) {
 #pragma unroll
     for (int i = 0; i < S; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][q][v] = 0.0f;
-      }
-    const uint32_t s = c.lds + (uint32_t)(slot * kStage);
+    v4u raw;
+    read_scales<S>(s, cur, ad, raw);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      f0.w[q] = lds_v4(s + ad.w + 2048 * q);
-      sw[q] = lds_u16(s + ad.sw + 128 * q);
-    }
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      f0.x[i] = lds_v4(s + ad.a0 + 2048 * i);
-      sx[i] = lds_u16(s + ad.sa + 128 * i);
-    }
+    for (int q = 0; q < S + 4; ++q) read_frag(f0, cur + ad.a[0], cur + ad.w, q);
+    shift_scales<S>(s, ad, raw);
   }
-  for (int j = 0; j < c.L.J; ++j) {
-    step<S>(c, k, ad, slot, acc, f0, f1, sx, sw);
-    slot = (slot + 1) & 3;
+  for (int d = 0; d < c.L.D; ++d) {
+    cur = wave_u32(c.lds + (uint32_t)(stage * kStage));
+    nxt = wave_u32(c.lds + (uint32_t)((stage ^ 1) * kStage));
+    step<S, 0>(c, k, ad, cur, nxt, acc, f0, f1, s);
+    step<S, 1>(c, k, ad, cur, nxt, acc, f0, f1, s);
+    stage ^= 1;
   }
   if constexpr (S > 0) {
     const int n = c.lane & 31, g = c.lane >> 5;
@@ -451,7 +511,7 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
 }
 
 template <bool kGlu, bool kF32>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void tiled_kernel(
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void tiled_kernel(
     Mx4Args a, Mx4Layout L, const int32_t* ws, int dense_tiles) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -473,41 +533,40 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   enter(c, k, first);
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   fetch_rows(c, first + c.stride);
-  for (int s = 0; s < kSlots; ++s) {
-    const uint32_t S = wave_u32(c.lds + (uint32_t)(s * kStage));
+  const uint32_t s0 = wave_u32(c.lds), s1 = wave_u32(c.lds + (uint32_t)kStage);
 #pragma unroll
-    for (int u = 0; u < kBlocks; ++u) issue1(c, k, S, __builtin_amdgcn_readfirstlane(k.j), u);
-    advance(c, k);
-  }
-  asm volatile("s_waitcnt vmcnt(30)\n\ts_barrier" ::: "memory");  // step 0 is there
+  for (int u = 0; u < 10; ++u) issue(c, k, s0, u);
+  advance(c, k);
+#pragma unroll
+  for (int u = 0; u < 6; ++u) issue(c, k, s1, u);
+  // stage 0 is there but for its second weights: they and six loads of stage 1 may be in flight
+  asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
 
   Addr ad;
   const int r = lane & 31, g = lane >> 5;
-  const uint32_t sz = (uint32_t)((r >> 2) & 3);
-  ad.w = opaque((uint32_t)(kA + 8192 * wn + 16 * lane));
-  ad.sw = opaque((uint32_t)(kA + kW + kSA + 512 * wn + 2 * lane));
-  int slot = 0;
+  const uint32_t sz = (uint32_t)((r >> 1) & 7);
+  ad.w = opaque((uint32_t)(kOffW + 8192 * wn + 16 * lane));
+  ad.sa = opaque((uint32_t)(kOffSA + 512 * wm + 16 * r));
+  ad.sw = opaque((uint32_t)(kOffSW + 1024 * wn + 16 * lane));
+  ad.shift = (uint32_t)(16 * g);
+  int stage = 0;
   for (int p = first; p < c.walk.hi; p += c.stride) {
     int tt, tn;
     walk_item(c.walk, p, tt, tn);
     const Tile t = get_tile(a, ws, tt, c.walk.ntt);
-    // the live sub-tiles in halves: the first wave row takes the odd one
-    const int n32 = (t.n + 31) / 32, h0 = (n32 + 1) / 2;
-    const int sub0 = wm == 0 ? 0 : h0, live = wm == 0 ? h0 : n32 - h0;
+    const int sub0 = first_sub(t.n, wm), live = sub_tiles(t.n, wm);
     const uint32_t row = (uint32_t)(32 * sub0 + r);
-    ad.a0 = opaque(row * 64 + (((uint32_t)(2 * g) ^ sz) << 4));
-    ad.a1 = opaque(row * 64 + (((uint32_t)(2 * g + 1) ^ sz) << 4));
-    ad.sa = opaque((uint32_t)(kA + kW) + row * 4 + 2 * g);
+#pragma unroll
+    for (int h = 0; h < 4; ++h)  // piece of K-half h % 2 of step h / 2
+      ad.a[h] = opaque(row * 128 + (((uint32_t)(4 * (h >> 1) + 2 * g + (h & 1)) ^ sz) << 4));
     const int group = tn * 2 + wn;
     switch (live) {
-      case 0: run_item<0, kGlu, kF32>(c, k, ad, slot, t, sub0, group); break;
-      case 1: run_item<1, kGlu, kF32>(c, k, ad, slot, t, sub0, group); break;
-      case 2: run_item<2, kGlu, kF32>(c, k, ad, slot, t, sub0, group); break;
-      case 3: run_item<3, kGlu, kF32>(c, k, ad, slot, t, sub0, group); break;
-      default: run_item<4, kGlu, kF32>(c, k, ad, slot, t, sub0, group); break;
+      case 0: run_item<0, kGlu, kF32>(c, k, ad, stage, t, sub0, group); break;
+      case 1: run_item<1, kGlu, kF32>(c, k, ad, stage, t, sub0, group); break;
+      default: run_item<2, kGlu, kF32>(c, k, ad, stage, t, sub0, group); break;
     }
   }
-  wait_vmcnt<0>();  // the dummy steps land before the LDS is given back
+  wait_vmcnt<0>();  // the dummy stages land before the LDS is given back
 }
 
 // CUs of the current device, a multiple of eight (one share per XCD).
@@ -538,7 +597,7 @@ hipError_t launch_mx4_tiled(const Mx4Args& a, const Mx4Layout& L, bool fp32_out,
     if (e != hipSuccess) return e;
   }
   const int dense_tiles = (a.P + kBM - 1) / kBM;
-  const dim3 grid((unsigned)workgroups()), block(256);
+  const dim3 grid((unsigned)workgroups()), block(64 * kWaves);
   if (L.glu) {
     if (fp32_out)
       hipLaunchKernelGGL((tiled_kernel<true, true>), grid, block, 0, st, a, L, list, dense_tiles);

@@ -73,7 +73,9 @@ def test_weight_sizes_and_refusals():
     assert p(1, 32, 128, 2) == 0 and p(1, 2 << 20, 128, 0) == 0
     for E, N, K, g in ((1, 32, 128, 0), (3, 96, 384, 0), (8, 64, 256, 1), (256, 7168, 2048, 0)):
         codes, scales = E * N * K // 2 << g, E * N * K // 32 << g
-        assert codes + scales <= p(E, N, K, g) <= codes + 2 * scales + 256
+        # (whole pairs of K-steps of 128; the scales for whole groups of four 32-row tiles)
+        even = (K + 255) // 256 * 256 / K
+        assert codes + scales <= p(E, N, K, g) <= (codes + 4 * scales) * even + 256
     d = _lib.MoeMxfp4Weights()
     f, D = L.moe_mxfp4_prepack, ctypes.byref(d)
     n = p(2, 64, 128, 0)
