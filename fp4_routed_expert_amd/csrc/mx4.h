@@ -121,7 +121,8 @@ struct Mx4Args {
   void* y;
 };
 hipError_t launch_mx4_stream(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, hipStream_t st);
-size_t mx4_tiled_ws_bytes(long P, int E);
+// (no workspace without offsets)
+size_t mx4_tiled_ws_bytes(long P, int E, int K);
 hipError_t launch_mx4_tiled(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, void* ws, hipStream_t st);
 
 // The norms' rows: what is read, what is written (null: not wanted).

@@ -160,7 +160,7 @@ moe_status_t moe_mxfp4_dense_forward(const moe_mxfp4_weights_t* w, const uint8_t
 
 size_t moe_mxfp4_grouped_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K, int32_t glu) {
   if (P < 0 || check_enk(E, N, K, glu) != MOE_OK) return 0;
-  return PackedLayout::align256(mx4_tiled_ws_bytes(P, E));
+  return PackedLayout::align256(mx4_tiled_ws_bytes(P, E, K));
 }
 
 moe_status_t moe_mxfp4_grouped_forward(const moe_mxfp4_weights_t* w, const uint8_t* xq, const uint8_t* xs, int32_t X,
@@ -178,7 +178,7 @@ moe_status_t moe_mxfp4_grouped_forward(const moe_mxfp4_weights_t* w, const uint8
   if (!xq || !xs || !offsets || !y) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(y, 16))
     return MOE_ERR_INVALID_ARGUMENT;
-  const size_t need = PackedLayout::align256(mx4_tiled_ws_bytes(P, w->E));
+  const size_t need = PackedLayout::align256(mx4_tiled_ws_bytes(P, w->E, w->K));
   if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
   const Mx4Layout L(w->E, w->N, w->K, w->glu != 0);

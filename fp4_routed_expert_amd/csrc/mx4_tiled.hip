@@ -46,7 +46,7 @@ constexpr int kSW = 2 * 1024;           // weight scales of two groups of four t
 constexpr int kOffW = kA, kOffSA = kA + 2 * kW, kOffSW = kOffSA + kSA;
 constexpr int kStage = kA + 2 * kW + kSA + kSW;
 constexpr int kIdx = 2 * kStage;        // LDS offset of the next item's row indices
-constexpr int kLds = kIdx + kWaves * 256 + kBM * 8;
+constexpr int kLds = kIdx + kWaves * 256;
 static_assert(kStage % 1024 == 0 && kLds <= 160 * 1024, "LDS");
 
 // One entry per 256 rows (at most) of a group, of equal heights.
@@ -59,9 +59,40 @@ __host__ __device__ __forceinline__ int tile_height(int n, int tiles) {
   return ((n + 31) / 32 + tiles - 1) / tiles * 32;
 }
 
-// ws: the number of tiles, then from byte 16 on four words per tile.
-__global__ __launch_bounds__(1024) void tiles_kernel(const int32_t* __restrict__ offsets, int E, int P, int cap,
-                                                     int32_t* __restrict__ ws) {
+// Workspace of a grouped product: the number of tiles, from byte 16 on four
+// words per tile, and from scales_at() on the activation scales by stage: the
+// eight bytes of stage d of sorted row p at 8 (d P + p), so that a tile's
+// scales of a stage are one run instead of a request to L2 for each row.
+long tile_cap(long P, int E) { return P / kBM + (P < E ? P : E); }
+size_t scales_at(long P, int E) { return PackedLayout::align256(16 + 16 * (size_t)tile_cap(P, E)); }
+
+// Block 0 lists the tiles, each thread of the others moves kPer stages of one
+// row's scales.
+constexpr int kPer = 8;
+__global__ __launch_bounds__(1024) void tiles_kernel(Mx4Args a, int E, int K, int cap, int32_t* __restrict__ ws,
+                                                     uint8_t* __restrict__ scales) {
+  const int P = a.P;
+  if (blockIdx.x > 0) {
+    const int D = (K + 255) / 256, nd = (D + kPer - 1) / kPer;
+    const size_t i = (size_t)(blockIdx.x - 1) * 1024 + threadIdx.x;
+    const size_t part = i / (size_t)P;
+    if (part >= (size_t)nd) return;
+    const int p = (int)(i - part * P), d0 = (int)part * kPer, n = min(kPer, D - d0);
+    int x = p;
+    if (a.rows) x = (int)((uint32_t)a.rows[p] / (uint32_t)a.div);
+    x = max(min(x, a.X - 1), 0);
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(a.xs + (size_t)x * (K / 32)) + 2 * d0;
+    const int dwords = K / 128 - 2 * d0;  // left in the row from stage d0 on
+    uint2 v[kPer];
+#pragma unroll
+    for (int d = 0; d < kPer; ++d)
+      if (d < n) v[d] = make_uint2(src[2 * d], src[min(2 * d + 1, dwords - 1)]);  // an odd number's last one twice
+#pragma unroll
+    for (int d = 0; d < kPer; ++d)
+      if (d < n) *reinterpret_cast<uint2*>(scales + 8 * ((size_t)(d0 + d) * P + p)) = v[d];
+    return;
+  }
+  const int32_t* offsets = a.offsets;
   __shared__ int wave_tot[16];
   const int e = threadIdx.x, lane = e & 63, w = e >> 6;
   int begin = 0, n = 0;
@@ -161,6 +192,10 @@ struct Ctx {
   const Mx4Args& a;
   const Mx4Layout& L;
   const int32_t* ws;
+  // activation scales: of sorted rows by stage (grouped), or of x by row (dense)
+  const uint8_t* scales;
+  uint32_t scale_row;  // bytes from a row
+  size_t scale_stage;  // and from a stage to the next
   Walk walk;
   int stride;  // of the walk
   uint32_t lds;
@@ -182,7 +217,7 @@ __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_
       "s_mov_b64 %0, %2\n\t"
       "global_load_lds_dwordx4 %1, %0 offset:%4"
       : "=&s"(t)
-      : "v"(off), "s"(base), "s"(lds), "n"(kOff)
+      : "v"(off), "s"(wave_ptr(base)), "s"(wave_u32(lds)), "n"(kOff)
       : "memory");
 }
 __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
@@ -192,7 +227,7 @@ __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t
       "s_mov_b64 %0, %2\n\t"
       "global_load_lds_dword %1, %0"
       : "=&s"(t)
-      : "v"(off), "s"(base), "s"(lds)
+      : "v"(off), "s"(wave_ptr(base)), "s"(wave_u32(lds))
       : "memory");
 }
 
@@ -213,24 +248,14 @@ __device__ __forceinline__ int scale_row(int n, int wave, int lane) {
 }
 
 // Row index DMA of item p (if there is one) into the index buffer: each wave
-// loads, and later reads, the indices of the rows whose pieces (32 of them) and
-// of those whose scales it moves.
+// loads, and later reads, the indices of the 32 rows whose pieces it moves.
 __device__ __forceinline__ void fetch_rows(const Ctx& c, int p) {
   if (!c.a.rows || p >= c.walk.hi) return;
   int tt, tn;
   walk_item(c.walk, p, tt, tn);
   const Tile t = get_tile(c.a, c.ws, tt, c.walk.ntt);
-  const uint8_t* base = wave_ptr(reinterpret_cast<const uint8_t*>(c.a.rows + t.row0));
-  const uint32_t at = wave_u32(c.lds + kIdx + 256u * (uint32_t)c.wave);
-  dma4(base, 4u * (uint32_t)min(32 * c.wave + (c.lane & 31), t.n - 1), at);
-  dma4(base, 4u * (uint32_t)min(scale_row(t.n, c.wave, c.lane), t.n - 1), at + 256u * kWaves);
-}
-
-// x row of row r of tile t; at: where the index buffer has its index.
-__device__ __forceinline__ uint32_t x_row(const Ctx& c, const Tile& t, int r, int at) {
-  int x = t.row0 + min(r, t.n - 1);  // rows past the tile read its last one
-  if (c.a.rows) x = (int)((uint32_t)lds_i32(c.lds + kIdx + 4 * at) / (uint32_t)c.a.div);
-  return (uint32_t)max(min(x, c.a.X - 1), 0);
+  dma4(wave_ptr(reinterpret_cast<const uint8_t*>(c.a.rows + t.row0)),
+       4u * (uint32_t)min(32 * c.wave + (c.lane & 31), t.n - 1), wave_u32(c.lds + kIdx + 256u * (uint32_t)c.wave));
 }
 
 // The last stage of an odd number of steps has no second step.  Its weights are
@@ -240,7 +265,7 @@ __device__ __forceinline__ void clip_tail(const Ctx& c, Cursor& k) {
   if (k.left != 1 || !(c.L.J & 1)) return;
 #pragma unroll
   for (int u = 0; u < 4; ++u) k.a[u] -= (((uint32_t)c.lane & 7) ^ (uint32_t)((c.lane >> 4) + 4 * (u & 1))) & 4 ? 64u : 0u;
-  k.sa -= 4u * (uint32_t)(c.lane & 1);
+  if (!c.a.offsets) k.sa -= 4u * (uint32_t)(c.lane & 1);
 }
 
 // Points the cursor at item p (whose row indices are in the index buffer).
@@ -254,12 +279,13 @@ __device__ __forceinline__ void enter(const Ctx& c, Cursor& k, int p) {
     const int r = 8 * u + (c.lane >> 3);
     // logical piece of the lane: physical piece l % 8 of a row whose r / 2 % 8 is l / 16 + 4 (u % 2)
     const uint32_t piece = ((uint32_t)c.lane & 7) ^ (uint32_t)((c.lane >> 4) + 4 * (u & 1));
-    k.a[u] = x_row(c, t, 32 * c.wave + r, 64 * c.wave + r) * ((uint32_t)L.K / 2) + 16u * piece;
+    int x = t.row0 + min(32 * c.wave + r, t.n - 1);  // rows past the tile read its last one
+    if (c.a.rows) x = (int)((uint32_t)lds_i32(c.lds + kIdx + 4 * (64 * c.wave + r)) / (uint32_t)c.a.div);
+    k.a[u] = (uint32_t)max(min(x, c.a.X - 1), 0) * ((uint32_t)L.K / 2) + 16u * piece;
   }
-  k.sa = x_row(c, t, scale_row(t.n, c.wave, c.lane), 64 * kWaves + 64 * c.wave + c.lane) * ((uint32_t)L.K / 32) +
-         4u * (uint32_t)(c.lane & 1);
+  k.sa = (uint32_t)min(scale_row(t.n, c.wave, c.lane), t.n - 1) * c.scale_row + 4u * (uint32_t)(c.lane & 1);
   k.x = wave_ptr(c.a.xq);
-  k.xs = wave_ptr(c.a.xs);
+  k.xs = wave_ptr(c.scales + (size_t)t.row0 * c.scale_row);
   // tiles past the last one read the last one; their columns are not stored
   k.w = wave_ptr(c.a.packed + L.tile_off(t.e, min(tn * kBT + c.wave, L.NT - 1)));
   k.ws = wave_ptr(c.a.packed + L.scale_off(t.e, min(2 * tn + (c.wave >> 2), L.NG - 1)) + 256 * (c.wave & 3));
@@ -294,7 +320,7 @@ __device__ __forceinline__ void advance(const Ctx& c, Cursor& k) {
     --k.left;
     k.x += 128;
     k.w += 4096;
-    k.xs += 8;
+    k.xs += c.scale_stage;
     k.ws += 1024;
     clip_tail(c, k);
     return;
@@ -512,12 +538,13 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
 
 template <bool kGlu, bool kF32>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void tiled_kernel(
-    Mx4Args a, Mx4Layout L, const int32_t* ws, int dense_tiles) {
+    Mx4Args a, Mx4Layout L, const int32_t* ws, const uint8_t* scales, int dense_tiles) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  Ctx c{a, L, ws, {}, (int)(gridDim.x >> 3), (uint32_t)(uintptr_t)(lds_u8*)lds, lane, wave};
+  Ctx c{a, L, ws, scales ? scales : a.xs, scales ? 8u : (uint32_t)L.K / 32, scales ? 8 * (size_t)a.P : 8, {},
+        (int)(gridDim.x >> 3), (uint32_t)(uintptr_t)(lds_u8*)lds, lane, wave};
   c.walk.ntt = a.offsets ? *reinterpret_cast<const cint*>(reinterpret_cast<uintptr_t>(ws)) : dense_tiles;
   c.walk.ntn = (L.NT + kBT - 1) / kBT;
   const int items = c.walk.ntt * c.walk.ntn, per = (items + 7) / 8;
@@ -583,16 +610,18 @@ int workgroups() {
   return n;
 }
 
-long tile_cap(long P, int E) { return P / kBM + (P < E ? P : E); }
-
 }  // namespace
 
-size_t mx4_tiled_ws_bytes(long P, int E) { return 16 + 16 * (size_t)tile_cap(P, E); }
+size_t mx4_tiled_ws_bytes(long P, int E, int K) { return scales_at(P, E) + 8 * (size_t)P * ((K + 255) / 256); }
 
 hipError_t launch_mx4_tiled(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, void* ws, hipStream_t st) {
   int32_t* list = static_cast<int32_t*>(ws);
+  uint8_t* scales = nullptr;
   if (a.offsets) {
-    hipLaunchKernelGGL(tiles_kernel, dim3(1), dim3(1024), 0, st, a.offsets, L.E, a.P, (int)tile_cap(a.P, L.E), list);
+    scales = static_cast<uint8_t*>(ws) + scales_at(a.P, L.E);
+    const size_t threads = (size_t)a.P * ((L.D + kPer - 1) / kPer);
+    hipLaunchKernelGGL(tiles_kernel, dim3((unsigned)(1 + (threads + 1023) / 1024)), dim3(1024), 0, st, a, L.E, L.K,
+                       (int)tile_cap(a.P, L.E), list, scales);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -600,14 +629,14 @@ hipError_t launch_mx4_tiled(const Mx4Args& a, const Mx4Layout& L, bool fp32_out,
   const dim3 grid((unsigned)workgroups()), block(64 * kWaves);
   if (L.glu) {
     if (fp32_out)
-      hipLaunchKernelGGL((tiled_kernel<true, true>), grid, block, 0, st, a, L, list, dense_tiles);
+      hipLaunchKernelGGL((tiled_kernel<true, true>), grid, block, 0, st, a, L, list, scales, dense_tiles);
     else
-      hipLaunchKernelGGL((tiled_kernel<true, false>), grid, block, 0, st, a, L, list, dense_tiles);
+      hipLaunchKernelGGL((tiled_kernel<true, false>), grid, block, 0, st, a, L, list, scales, dense_tiles);
   } else {
     if (fp32_out)
-      hipLaunchKernelGGL((tiled_kernel<false, true>), grid, block, 0, st, a, L, list, dense_tiles);
+      hipLaunchKernelGGL((tiled_kernel<false, true>), grid, block, 0, st, a, L, list, scales, dense_tiles);
     else
-      hipLaunchKernelGGL((tiled_kernel<false, false>), grid, block, 0, st, a, L, list, dense_tiles);
+      hipLaunchKernelGGL((tiled_kernel<false, false>), grid, block, 0, st, a, L, list, scales, dense_tiles);
   }
   return hipGetLastError();
 }
