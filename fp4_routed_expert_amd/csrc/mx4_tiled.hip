@@ -454,40 +454,56 @@ __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, ui
   }
 }
 
-// Stores of a wave's S sub-tiles: element v of a lane is row 8 (v / 4) + 4 g +
-// v % 4 of its sub-tile; the group's f tiles are f neighbouring columns, so a
-// half-wave's store covers a whole run of 128 (64 with SwiGLU) outputs.
-template <bool kGlu, bool kF32>
-__device__ __forceinline__ void store_row(const Ctx& c, const float (&v)[4], size_t row, int group, int f, int n) {
+// SiLU(g) u for the SwiGLU epilogue, as silu_mul but with the exponential
+// straight from the exp2 instruction (whose results below 2^-126 are 0 here,
+// as 1 + them is 1 anyway).
+__device__ __forceinline__ float glu_out(float g, float u) {
+  return g * u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+}
+
+// Stores of one sub-tile: element v of a lane is row 8 (v / 4) + 4 g + v % 4;
+// the group's f tiles are f neighbouring columns, so a half-wave's store covers
+// a whole run of 128 (64 with SwiGLU) outputs.  base (uniform): row 0 of the
+// sub-tile, the group's first column; off: the lane's bytes from there (its
+// column, and 4 g rows down); left: rows of the sub-tile that exist.
+template <bool kGlu, bool kF32, bool kMask>
+__device__ __forceinline__ void store_sub(const v16f (&acc)[4], uint8_t* base, size_t row_bytes, uint32_t off, int left,
+                                          int f) {
   constexpr int kO = kGlu ? 2 : 4;
-  float o[kO];
 #pragma unroll
-  for (int t = 0; t < kO; ++t) o[t] = kGlu ? silu_mul(v[2 * t], v[2 * t + 1]) : v[t];
-  const size_t at = row * c.L.N + 32 * kO * group + f * n;
-  if constexpr (kF32) {
-    float* y = static_cast<float*>(c.a.y) + at;
-    if (f == kO) {
-      if constexpr (kGlu)
-        *reinterpret_cast<v2f*>(y) = v2f{o[0], o[1]};
-      else
-        *reinterpret_cast<v4f*>(y) = v4f{o[0], o[1], o[2], o[3]};
-    } else {
+  for (int v = 0; v < 16; ++v) {
+    uint8_t* y = base + (size_t)(8 * (v >> 2) + (v & 3)) * row_bytes + off;
+    float o[kO];
 #pragma unroll
-      for (int t = 0; t < kO - 1; ++t)
-        if (t < f) y[t] = o[t];
+    for (int t = 0; t < kO; ++t) o[t] = kGlu ? glu_out(acc[2 * t][v], acc[2 * t + 1][v]) : acc[t][v];
+    if (!kMask || 8 * (v >> 2) + (v & 3) < left) {  // left: less the lane's 4 g
+      if constexpr (kF32) {
+        float* q = reinterpret_cast<float*>(y);
+        if (!kMask || f == kO) {
+          if constexpr (kGlu)
+            *reinterpret_cast<v2f*>(q) = v2f{o[0], o[1]};
+          else
+            *reinterpret_cast<v4f*>(q) = v4f{o[0], o[1], o[2], o[3]};
+        } else {
+#pragma unroll
+          for (int t = 0; t < kO - 1; ++t)
+            if (t < f) q[t] = o[t];
+        }
+      } else {
+        uint16_t* q = reinterpret_cast<uint16_t*>(y);
+        if (!kMask || f == kO) {
+          if constexpr (kGlu)
+            *reinterpret_cast<uint32_t*>(q) = f32x2_to_bf16(o[0], o[1]);
+          else
+            *reinterpret_cast<uint2*>(q) = make_uint2(f32x2_to_bf16(o[0], o[1]), f32x2_to_bf16(o[2], o[3]));
+        } else {
+#pragma unroll
+          for (int t = 0; t < kO - 1; ++t)
+            if (t < f) q[t] = f32_to_bf16(o[t]);
+        }
+      }
     }
-  } else {
-    uint16_t* y = static_cast<uint16_t*>(c.a.y) + at;
-    if (f == kO) {
-      if constexpr (kGlu)
-        *reinterpret_cast<uint32_t*>(y) = f32x2_to_bf16(o[0], o[1]);
-      else
-        *reinterpret_cast<uint2*>(y) = make_uint2(f32x2_to_bf16(o[0], o[1]), f32x2_to_bf16(o[2], o[3]));
-    } else {
-#pragma unroll
-      for (int t = 0; t < kO - 1; ++t)
-        if (t < f) y[t] = f32_to_bf16(o[t]);
-    }
+    if ((v & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // four rows at a time out of the accumulators
   }
 }
 
@@ -519,19 +535,20 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
     stage ^= 1;
   }
   if constexpr (S > 0) {
-    const int n = c.lane & 31, g = c.lane >> 5;
     constexpr int kO = kGlu ? 2 : 4;
-    const int left = c.L.N / 32 - kO * group, f = left < kO ? left : kO;
-    if (f > 0) {
+    constexpr uint32_t kB = kF32 ? 4 : 2;
+    const int g = c.lane >> 5, left = c.L.N / 32 - kO * group, f = min(left, kO);
+    const size_t row_bytes = (size_t)c.L.N * kB;
+    const uint32_t off = ((uint32_t)(4 * g) * (uint32_t)c.L.N + (uint32_t)f * (uint32_t)(c.lane & 31)) * kB;
 #pragma unroll
-      for (int i = 0; i < S; ++i)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int m = 32 * (sub0 + i) + 8 * (v >> 2) + 4 * g + (v & 3);
-          const float o[4] = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
-          if (m < t.n) store_row<kGlu, kF32>(c, o, (size_t)t.row0 + m, group, f, n);
-          __builtin_amdgcn_sched_barrier(0);  // one row at a time out of the accumulators
-        }
+    for (int i = 0; i < S; ++i) {
+      const int m = 32 * (sub0 + i);
+      uint8_t* base = static_cast<uint8_t*>(c.a.y) + ((size_t)(t.row0 + m) * c.L.N + (size_t)(32 * kO) * group) * kB;
+      base = const_cast<uint8_t*>(wave_ptr(base));
+      if (f == kO && m + 32 <= t.n)
+        store_sub<kGlu, kF32, false>(acc[i], base, row_bytes, off, 32, f);
+      else if (f > 0)
+        store_sub<kGlu, kF32, true>(acc[i], base, row_bytes, off, t.n - m - 4 * g, f);
     }
   }
 }
