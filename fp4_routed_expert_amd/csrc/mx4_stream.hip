@@ -64,22 +64,25 @@ __device__ __forceinline__ void load_step(Step<NT>& p, const uint8_t* const (&wt
     p.w[t][0] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(w));
     p.w[t][1] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(w + 1024));
   }
-  p.sw = *reinterpret_cast<const uint32_t*>(st + (size_t)(j >> 1) * 1024 + 8 * (j & 1));
+  const uint8_t* sc = st + (size_t)(j >> 1) * 1024 + 8 * (j & 1);
+  p.sw = NT == 2 ? *reinterpret_cast<const uint32_t*>(sc) : *reinterpret_cast<const uint16_t*>(sc);
   p.x[0] = *reinterpret_cast<const v4u*>(xrow + (size_t)j * 64);
   p.x[1] = *reinterpret_cast<const v4u*>(xrow + (size_t)j * 64 + 16);
   p.sx = *reinterpret_cast<const uint16_t*>(xscale + (size_t)j * 4);
 }
 
-__device__ __forceinline__ void multiply(const Step<2>& p, v16f (&acc)[2]) {
+// sw holds tile t's scale bytes at 2 t (NT = 1: at 0)
+template <int NT>
+__device__ __forceinline__ void multiply(const Step<NT>& p, v16f (&acc)[NT]) {
   acc[0] = mfma_fp4<0, 0>(p.x[0], p.w[0][0], acc[0], p.sx, p.sw);
-  acc[1] = mfma_fp4<0, 2>(p.x[0], p.w[1][0], acc[1], p.sx, p.sw);
+  if constexpr (NT == 2) acc[1] = mfma_fp4<0, 2>(p.x[0], p.w[1][0], acc[1], p.sx, p.sw);
   acc[0] = mfma_fp4<1, 1>(p.x[1], p.w[0][1], acc[0], p.sx, p.sw);
-  acc[1] = mfma_fp4<1, 3>(p.x[1], p.w[1][1], acc[1], p.sx, p.sw);
+  if constexpr (NT == 2) acc[1] = mfma_fp4<1, 3>(p.x[1], p.w[1][1], acc[1], p.sx, p.sw);
 }
 
-template <int NW, int kB, bool kGlu, bool kF32>
+template <int NW, int NT, int kB, bool kGlu, bool kF32>
 __global__ __launch_bounds__(64 * NW) void stream_kernel(Mx4Args a, Mx4Layout L) {
-  constexpr int NT = 2;
+  static_assert(NT == 2 || (NT == 1 && !kGlu), "a gate tile with its up tile");
   __shared__ v4f red[NW][NT * 4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = lane & 31, g = lane >> 5;
@@ -123,11 +126,11 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(Mx4Args a, Mx4Layout L)
 #pragma unroll
       for (int b = 0; b < kB; ++b) load_step<NT>(p[b], wt, st, xrow, xscale, wave + NW * (u + b));
 #pragma unroll
-      for (int b = 0; b < kB; ++b) multiply(p[b], acc);
+      for (int b = 0; b < kB; ++b) multiply<NT>(p[b], acc);
     }
     for (; u < nsteps; ++u) {
       load_step<NT>(p[0], wt, st, xrow, xscale, wave + NW * u);
-      multiply(p[0], acc);
+      multiply<NT>(p[0], acc);
     }
     // element v of a lane is token 8 (v / 4) + 4 g + v % 4: only the groups of
     // eight tokens that exist are joined
@@ -168,20 +171,13 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(Mx4Args a, Mx4Layout L)
   }
 }
 
-template <int NW, int kB>
+template <int NW, int NT, int kB, bool kGlu>
 void stream_as(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, hipStream_t st) {
-  const dim3 grid((unsigned)((L.NT + 1) / 2), a.offsets ? (unsigned)L.E : (unsigned)min((a.P + kRows - 1) / kRows, 65535));
-  if (L.glu) {
-    if (fp32_out)
-      hipLaunchKernelGGL((stream_kernel<NW, kB, true, true>), grid, dim3(64 * NW), 0, st, a, L);
-    else
-      hipLaunchKernelGGL((stream_kernel<NW, kB, true, false>), grid, dim3(64 * NW), 0, st, a, L);
-  } else {
-    if (fp32_out)
-      hipLaunchKernelGGL((stream_kernel<NW, kB, false, true>), grid, dim3(64 * NW), 0, st, a, L);
-    else
-      hipLaunchKernelGGL((stream_kernel<NW, kB, false, false>), grid, dim3(64 * NW), 0, st, a, L);
-  }
+  const dim3 grid((unsigned)((L.NT + NT - 1) / NT), a.offsets ? (unsigned)L.E : (unsigned)min((a.P + kRows - 1) / kRows, 65535));
+  if (fp32_out)
+    hipLaunchKernelGGL((stream_kernel<NW, NT, kB, kGlu, true>), grid, dim3(64 * NW), 0, st, a, L);
+  else
+    hipLaunchKernelGGL((stream_kernel<NW, NT, kB, kGlu, false>), grid, dim3(64 * NW), 0, st, a, L);
 }
 
 }  // namespace
@@ -194,10 +190,23 @@ hipError_t launch_mx4_pack(const uint8_t* wq, const uint8_t* ws, const uint8_t* 
 }
 
 hipError_t launch_mx4_stream(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, hipStream_t st) {
-  if (L.J >= 32)
-    stream_as<8, 2>(a, L, fp32_out, st);
-  else
-    stream_as<4, 2>(a, L, fp32_out, st);
+  const long groups = a.offsets ? L.E : (a.P + kRows - 1) / kRows;
+  if (L.glu) {
+    if (L.J >= 64)
+      stream_as<8, 2, 2, true>(a, L, fp32_out, st);
+    else
+      stream_as<4, 2, 2, true>(a, L, fp32_out, st);
+  } else if (groups * ((L.NT + 1) / 2) < 512) {
+    if (L.J >= 64)
+      stream_as<16, 1, 2, false>(a, L, fp32_out, st);
+    else
+      stream_as<8, 1, 2, false>(a, L, fp32_out, st);
+  } else {
+    if (L.J >= 64)
+      stream_as<8, 2, 2, false>(a, L, fp32_out, st);
+    else
+      stream_as<4, 2, 2, false>(a, L, fp32_out, st);
+  }
   return hipGetLastError();
 }
 

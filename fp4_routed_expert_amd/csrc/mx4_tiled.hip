@@ -461,41 +461,47 @@ __device__ __forceinline__ float glu_out(float g, float u) {
   return g * u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
+// Global (not flat) pointers: flat stores would count as LDS traffic too.
+template <class T>
+using global = __attribute__((address_space(1))) T;
+typedef global<uint8_t> gbyte;
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
 // Stores of one sub-tile: element v of a lane is row 8 (v / 4) + 4 g + v % 4;
 // the group's f tiles are f neighbouring columns, so a half-wave's store covers
 // a whole run of 128 (64 with SwiGLU) outputs.  base (uniform): row 0 of the
 // sub-tile, the group's first column; off: the lane's bytes from there (its
 // column, and 4 g rows down); left: rows of the sub-tile that exist.
 template <bool kGlu, bool kF32, bool kMask>
-__device__ __forceinline__ void store_sub(const v16f (&acc)[4], uint8_t* base, size_t row_bytes, uint32_t off, int left,
+__device__ __forceinline__ void store_sub(const v16f (&acc)[4], gbyte* base, size_t row_bytes, uint32_t off, int left,
                                           int f) {
   constexpr int kO = kGlu ? 2 : 4;
 #pragma unroll
   for (int v = 0; v < 16; ++v) {
-    uint8_t* y = base + (size_t)(8 * (v >> 2) + (v & 3)) * row_bytes + off;
+    gbyte* y = base + (size_t)(8 * (v >> 2) + (v & 3)) * row_bytes + off;
     float o[kO];
 #pragma unroll
     for (int t = 0; t < kO; ++t) o[t] = kGlu ? glu_out(acc[2 * t][v], acc[2 * t + 1][v]) : acc[t][v];
     if (!kMask || 8 * (v >> 2) + (v & 3) < left) {  // left: less the lane's 4 g
       if constexpr (kF32) {
-        float* q = reinterpret_cast<float*>(y);
+        global<float>* q = reinterpret_cast<global<float>*>(y);
         if (!kMask || f == kO) {
           if constexpr (kGlu)
-            *reinterpret_cast<v2f*>(q) = v2f{o[0], o[1]};
+            *reinterpret_cast<global<v2f>*>(q) = v2f{o[0], o[1]};
           else
-            *reinterpret_cast<v4f*>(q) = v4f{o[0], o[1], o[2], o[3]};
+            *reinterpret_cast<global<v4f>*>(q) = v4f{o[0], o[1], o[2], o[3]};
         } else {
 #pragma unroll
           for (int t = 0; t < kO - 1; ++t)
             if (t < f) q[t] = o[t];
         }
       } else {
-        uint16_t* q = reinterpret_cast<uint16_t*>(y);
+        global<uint16_t>* q = reinterpret_cast<global<uint16_t>*>(y);
         if (!kMask || f == kO) {
           if constexpr (kGlu)
-            *reinterpret_cast<uint32_t*>(q) = f32x2_to_bf16(o[0], o[1]);
+            *reinterpret_cast<global<uint32_t>*>(q) = f32x2_to_bf16(o[0], o[1]);
           else
-            *reinterpret_cast<uint2*>(q) = make_uint2(f32x2_to_bf16(o[0], o[1]), f32x2_to_bf16(o[2], o[3]));
+            *reinterpret_cast<global<v2u>*>(q) = v2u{f32x2_to_bf16(o[0], o[1]), f32x2_to_bf16(o[2], o[3])};
         } else {
 #pragma unroll
           for (int t = 0; t < kO - 1; ++t)
@@ -544,11 +550,11 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
     for (int i = 0; i < S; ++i) {
       const int m = 32 * (sub0 + i);
       uint8_t* base = static_cast<uint8_t*>(c.a.y) + ((size_t)(t.row0 + m) * c.L.N + (size_t)(32 * kO) * group) * kB;
-      base = const_cast<uint8_t*>(wave_ptr(base));
+      gbyte* gb = reinterpret_cast<gbyte*>(reinterpret_cast<uintptr_t>(wave_ptr(base)));
       if (f == kO && m + 32 <= t.n)
-        store_sub<kGlu, kF32, false>(acc[i], base, row_bytes, off, 32, f);
+        store_sub<kGlu, kF32, false>(acc[i], gb, row_bytes, off, 32, f);
       else if (f > 0)
-        store_sub<kGlu, kF32, true>(acc[i], base, row_bytes, off, t.n - m - 4 * g, f);
+        store_sub<kGlu, kF32, true>(acc[i], gb, row_bytes, off, t.n - m - 4 * g, f);
     }
   }
 }

@@ -9,7 +9,6 @@ keep allocation out of the call.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 
@@ -25,7 +24,7 @@ _NORM_DTYPES = (torch.bfloat16, torch.float32)
 def _need(t: torch.Tensor, name: str, dtypes, shape, dev=None):
     """Type, shape and device of a contiguous argument; its address."""
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_contiguous():
@@ -35,13 +34,20 @@ def _need(t: torch.Tensor, name: str, dtypes, shape, dev=None):
     return t.data_ptr()
 
 
-def _on(dev: torch.device):
-    """The tensors' device as the current one, as the library's launches need it."""
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+# The current stream's handle without a Stream object around it, where torch has it.
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+def _call(name: str, dev: torch.device, *args):
+    """One library call on dev's current stream, dev being the current device meanwhile."""
+    fn = getattr(_lib.lib(), name)
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, _stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(dev.index))
+    if status:
+        _lib.check(status, name)
 
 
 def _u8(t, name, shape, dev):
@@ -74,9 +80,7 @@ def quant_mxfp4(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tensor 
     if s is None:
         s = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
     qp, sp = _u8(q, "q", (M, K // 2), dev), _u8(s, "s", (M, K // 32), dev)
-    with _on(dev):
-        _lib.check(_lib.lib().moe_quant_mxfp4(x.data_ptr(), _TYPES[x.dtype], M, K, x.stride(0) if M > 1 else K, qp, sp,
-                                              _stream(dev)), "moe_quant_mxfp4")
+    _call("moe_quant_mxfp4", dev, x.data_ptr(), _TYPES[x.dtype], M, K, x.stride(0) if M > 1 else K, qp, sp)
     return q, s
 
 
@@ -92,9 +96,7 @@ def dequant_mx(q: torch.Tensor, s: torch.Tensor, format: str, dtype: torch.dtype
         out = torch.empty((M, K), dtype=dtype, device=dev)
     qp = _u8(q, "q", (M, K // 2 if format == "mxfp4" else K), None)
     sp, op = _u8(s, "s", (M, K // 32), dev), _need(out, "out", _TYPES, (M, K), dev)
-    with _on(dev):
-        _lib.check(_lib.lib().moe_dequant_mx(qp, sp, _QUANT[format], M, K, op, _TYPES[out.dtype], _stream(dev)),
-                   "moe_dequant_mx")
+    _call("moe_dequant_mx", dev, qp, sp, _QUANT[format], M, K, op, _TYPES[out.dtype])
     return out
 
 
@@ -131,15 +133,12 @@ def _prepack(wq, ws, uq, us) -> Mxfp4Weights:
     ptr = [_u8(wq, "wq", wq.shape, None), _u8(ws, "ws", sshape, dev), None, None]
     if uq is not None:
         ptr[2:] = [_u8(uq, "uq", wq.shape, dev), _u8(us, "us", sshape, dev)]
-    L = _lib.lib()
-    nbytes = L.moe_mxfp4_packed_bytes(E, N, K, int(uq is not None))
+    nbytes = _lib.lib().moe_mxfp4_packed_bytes(E, N, K, int(uq is not None))
     if nbytes == 0:
         raise _lib.MoeError(_lib.MOE_ERR_UNSUPPORTED, "moe_mxfp4_packed_bytes")
     buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     desc = _lib.MoeMxfp4Weights()
-    with _on(dev):
-        _lib.check(L.moe_mxfp4_prepack(*ptr, E, N, K, buf.data_ptr(), nbytes, ctypes.byref(desc), _stream(dev)),
-                   "moe_mxfp4_prepack")
+    _call("moe_mxfp4_prepack", dev, *ptr, E, N, K, buf.data_ptr(), nbytes, ctypes.byref(desc))
     return Mxfp4Weights(buffer=buf, desc=desc)
 
 
@@ -162,9 +161,7 @@ def mxfp4_dense(w: Mxfp4Weights, xq: torch.Tensor, xs: torch.Tensor, dtype: torc
         y = torch.empty((T, w.N), dtype=dtype, device=dev)
     xp, sp = _u8(xq, "xq", (T, w.K // 2), w.buffer.device), _u8(xs, "xs", (T, w.K // 32), dev)
     yp = _need(y, "y", _NORM_DTYPES, (T, w.N), dev)
-    with _on(dev):
-        _lib.check(_lib.lib().moe_mxfp4_dense_forward(ctypes.byref(w.desc), xp, sp, T, yp, _TYPES[y.dtype], flags,
-                                                      _stream(dev)), "moe_mxfp4_dense_forward")
+    _call("moe_mxfp4_dense_forward", dev, ctypes.byref(w.desc), xp, sp, T, yp, _TYPES[y.dtype], flags)
     return y
 
 
@@ -187,10 +184,8 @@ def mxfp4_grouped(w: Mxfp4Weights, xq: torch.Tensor, xs: torch.Tensor, offsets: 
     rp = None if rows is None else _need(rows, "rows", (torch.int32,), (P,), dev)
     yp = _need(y, "y", _NORM_DTYPES, (P, w.N), dev)
     workspace = _workspace(workspace, lambda: mxfp4_grouped_workspace_size(P, w.E, w.N, w.K, w.glu), dev)
-    with _on(dev):
-        _lib.check(_lib.lib().moe_mxfp4_grouped_forward(
-            ctypes.byref(w.desc), xp, sp, X, op, rp, row_div, P, yp, _TYPES[y.dtype], workspace.data_ptr(),
-            workspace.numel(), flags, _stream(dev)), "moe_mxfp4_grouped_forward")
+    _call("moe_mxfp4_grouped_forward", dev, ctypes.byref(w.desc), xp, sp, X, op, rp, row_div, P, yp, _TYPES[y.dtype],
+          workspace.data_ptr(), workspace.numel(), flags)
     return y
 
 
@@ -225,9 +220,7 @@ def norm_before(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, quant:
     xp = _need(x, "x", _NORM_DTYPES, (T, H), None)
     wp = _need(weight, "weight", _NORM_DTYPES, (H,), dev)
     z, q, s, out = _norm_outputs(T, H, dev, quant, z, q, s, want_z)
-    with _on(dev):
-        _lib.check(_lib.lib().moe_norm_before(xp, _TYPES[x.dtype], wp, _TYPES[weight.dtype], T, H, eps, *out,
-                                              _QUANT[quant], _stream(dev)), "moe_norm_before")
+    _call("moe_norm_before", dev, xp, _TYPES[x.dtype], wp, _TYPES[weight.dtype], T, H, eps, *out, _QUANT[quant])
     return z, q, s
 
 
@@ -276,10 +269,8 @@ def norm_after(y: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor | N
     if next_weight is None and (quant is not None or z is not None):
         raise ValueError("z and quant need next_weight")
     z, q, s, ptr = _norm_outputs(T, H, dev, quant, z, q, s, want_z and next_weight is not None)
-    with _on(dev):
-        _lib.check(_lib.lib().moe_norm_after(
-            yp, _TYPES[y.dtype], rp, _TYPES[residual.dtype], wp, np_, w_type, gp, gate_t, gate_h, alpha, beta, eps, T,
-            H, op, *ptr, _QUANT[quant], _stream(dev)), "moe_norm_after")
+    _call("moe_norm_after", dev, yp, _TYPES[y.dtype], rp, _TYPES[residual.dtype], wp, np_, w_type, gp, gate_t, gate_h,
+          alpha, beta, eps, T, H, op, *ptr, _QUANT[quant])
     return out, z, q, s
 
 
@@ -306,8 +297,6 @@ def block_forward(pw, n_shared: int, router_w: torch.Tensor, x: torch.Tensor, k:
     gp, gate_t, gate_h = _gate(gate, T, H, dev)
     norms = _lib.MoeBlockNorms(pre, post, w_type, gp, gate_t, gate_h, alpha, beta, eps)
     workspace = _workspace(workspace, lambda: block_workspace_size(T, pw.E, k, H, pw.I, n_shared, flags), dev)
-    with _on(dev):
-        _lib.check(_lib.lib().moe_fp4_block_forward(
-            ctypes.byref(pw.desc), n_shared, wp, ctypes.byref(norms), xp, _TYPES[x.dtype], T, k, op,
-            workspace.data_ptr(), workspace.numel(), flags, _stream(dev)), "moe_fp4_block_forward")
+    _call("moe_fp4_block_forward", dev, ctypes.byref(pw.desc), n_shared, wp, ctypes.byref(norms), xp, _TYPES[x.dtype], T,
+          k, op, workspace.data_ptr(), workspace.numel(), flags)
     return out
