@@ -46,7 +46,9 @@ constexpr int kSW = 2 * 1024;           // weight scales of two groups of four t
 constexpr int kOffW = kA, kOffSA = kA + 2 * kW, kOffSW = kOffSA + kSA;
 constexpr int kStage = kA + 2 * kW + kSA + kSW;
 constexpr int kIdx = 2 * kStage;        // LDS offset of the next item's row indices
-constexpr int kLds = kIdx + kWaves * 256;
+constexpr int kInfo = kIdx + kWaves * 256;   // for each wave eight items' (first row, rows, column)
+constexpr int kState = kInfo + kWaves * 128; // and where its cursor goes next
+constexpr int kLds = kState + kWaves * 64;
 static_assert(kStage % 1024 == 0 && kLds <= 160 * 1024, "LDS");
 
 // One entry per 256 rows (at most) of a group, of equal heights.
@@ -60,17 +62,19 @@ __host__ __device__ __forceinline__ int tile_height(int n, int tiles) {
 }
 
 // Workspace of a grouped product: the number of tiles, from byte 16 on four
-// words per tile, and from scales_at() on the activation scales by stage: the
-// eight bytes of stage d of sorted row p at 8 (d P + p), so that a tile's
-// scales of a stage are one run instead of a request to L2 for each row.
+// words per tile, from rows_at() on the x row of each sorted row, and from
+// scales_at() on the activation scales by stage: the eight bytes of stage d of
+// sorted row p at 8 (d P + p), so that a tile's scales of a stage are one run
+// instead of a request to L2 for each row.
 long tile_cap(long P, int E) { return P / kBM + (P < E ? P : E); }
-size_t scales_at(long P, int E) { return PackedLayout::align256(16 + 16 * (size_t)tile_cap(P, E)); }
+size_t rows_at(long P, int E) { return PackedLayout::align256(16 + 16 * (size_t)tile_cap(P, E)); }
+size_t scales_at(long P, int E) { return PackedLayout::align256(rows_at(P, E) + 4 * (size_t)P); }
 
 // Block 0 lists the tiles, each thread of the others moves kPer stages of one
 // row's scales.
 constexpr int kPer = 8;
 __global__ __launch_bounds__(1024) void tiles_kernel(Mx4Args a, int E, int K, int cap, int32_t* __restrict__ ws,
-                                                     uint8_t* __restrict__ scales) {
+                                                     int32_t* __restrict__ xrows, uint8_t* __restrict__ scales) {
   const int P = a.P;
   if (blockIdx.x > 0) {
     const int D = (K + 255) / 256, nd = (D + kPer - 1) / kPer;
@@ -81,6 +85,7 @@ __global__ __launch_bounds__(1024) void tiles_kernel(Mx4Args a, int E, int K, in
     int x = p;
     if (a.rows) x = (int)((uint32_t)a.rows[p] / (uint32_t)a.div);
     x = max(min(x, a.X - 1), 0);
+    if (a.rows && d0 == 0) xrows[p] = x;
     const uint32_t* src = reinterpret_cast<const uint32_t*>(a.xs + (size_t)x * (K / 32)) + 2 * d0;
     const int dwords = K / 128 - 2 * d0;  // left in the row from stage d0 on
     uint2 v[kPer];
@@ -118,36 +123,71 @@ __global__ __launch_bounds__(1024) void tiles_kernel(Mx4Args a, int E, int K, in
 
 typedef __attribute__((address_space(4))) const int32_t cint;  // read by scalar loads
 
-// Position p of the walk -> the item's tile of rows and its first weight tile.
-struct Walk {
-  int ntt, ntn;  // row tiles, weight-tile columns of eight
-  int lo, hi;    // this XCD's share
+// What a launch is given.  Only a few of these values are needed at every
+// stage; the others are read again from the kernel's arguments (by scalar
+// loads) where an item begins or ends, since scalar registers that are kept
+// over the K loop spill, and vector registers with them.
+struct Launch {
+  Mx4Args a;
+  Mx4Layout L;
+  const int32_t* ws;      // tile list (grouped)
+  const int32_t* xrows;   // x row of each sorted row, or null: the same row
+  const uint8_t* scales;  // activation scales: of sorted rows by stage (grouped), or of x by row (dense)
+  size_t scale_stage;     // bytes from a stage to the next
+  int scale_row;          // and from a row to the next
+  int tiles, height;      // dense: row tiles and their height
 };
+typedef __attribute__((address_space(4))) const Launch claunch;
 
-__device__ __forceinline__ void walk_item(const Walk& k, int p, int& tt, int& tn) {
-  // panels of a quarter of the columns, row tiles running inside a panel: the
-  // items that an XCD holds at one time share rows and weights in its L2
-  const int sn = (k.ntn + 3) / 4;
-  const int sc = p / (k.ntt * sn), q = p - sc * (k.ntt * sn);
-  const int w = min(sn, k.ntn - sc * sn);
-  tt = q / w;
-  tn = sc * sn + q % w;
+// Where a wave's walk over the items stands (in LDS between items).  The items
+// go by panels of a quarter of the columns, row tiles running inside a panel,
+// so that the items that an XCD holds at one time share rows and weights in
+// its L2.  Steps inside a panel need no division.
+struct Walk {
+  int p, hi, stride;  // item, end of this XCD's share, items from one to the next
+  int ntt, ntn;       // row tiles, weight-tile columns of eight
+  int tt, off;        // row tile, column inside the panel
+  int base, w;        // the panel's first column and its width
+  int st, so;         // stride / w, stride % w
+  int e, row0, n;     // the item's tile of rows
+  int count, more;    // items before it; whether there is one
+};
+static_assert(sizeof(Walk) == 64, "four 128-bit words");
+
+__device__ __forceinline__ void locate(Walk& k) {
+  const int sn = (k.ntn + 3) / 4, sc = k.p / (k.ntt * sn), q = k.p - sc * (k.ntt * sn);
+  k.base = sc * sn;
+  k.w = max(min(sn, k.ntn - k.base), 1);
+  k.tt = q / k.w;
+  k.off = q - k.tt * k.w;
+  k.st = k.stride / k.w;
+  k.so = k.stride - k.st * k.w;
 }
-
-__device__ __forceinline__ Tile get_tile(const Mx4Args& a, const int32_t* ws, int tt, int ntt) {
-  Tile t;
-  if (a.offsets) {
-    const cint* p = reinterpret_cast<const cint*>(reinterpret_cast<uintptr_t>(ws)) + 4 + 4 * tt;
-    t.e = p[0];
-    t.row0 = p[1];
-    t.n = p[2];
+__device__ __forceinline__ void look_up(const claunch* g, Walk& k) {
+  if (g->a.offsets) {
+    const cint* p = reinterpret_cast<const cint*>(reinterpret_cast<uintptr_t>(g->ws)) + 4 + 4 * k.tt;
+    k.e = p[0];
+    k.row0 = p[1];
+    k.n = p[2];
   } else {
-    const int h = tile_height(a.P, ntt);
-    t.e = 0;
-    t.row0 = tt * h;
-    t.n = min(h, a.P - t.row0);
+    k.e = 0;
+    k.row0 = k.tt * g->height;
+    k.n = min(g->height, g->a.P - k.row0);
   }
-  return t;
+}
+__device__ __forceinline__ void next_item(const claunch* g, Walk& k) {
+  k.p += k.stride;
+  ++k.count;
+  k.more = k.p < k.hi;
+  if (!k.more) return;
+  k.tt += k.st;
+  k.off += k.so;
+  if (k.off >= k.w) {
+    k.off -= k.w;
+    ++k.tt;
+  }
+  if (k.tt >= k.ntt) locate(k);
+  look_up(g, k);
 }
 
 __device__ __forceinline__ uint32_t opaque(uint32_t x) {
@@ -181,7 +221,7 @@ struct Cursor {
   const uint8_t* ws;  // the wave's part of the weight scales
   uint32_t a[4];      // per lane: its piece of rows 32 w + 8 u + l / 8
   uint32_t sa;        // per lane: its dword of row scales
-  int p, left;        // item, stages left of it (this one counted)
+  int left;           // stages left of the item (this one counted)
 };
 
 struct Frag {
@@ -189,17 +229,19 @@ struct Frag {
 };
 
 struct Ctx {
-  const Mx4Args& a;
-  const Mx4Layout& L;
-  const int32_t* ws;
-  // activation scales: of sorted rows by stage (grouped), or of x by row (dense)
-  const uint8_t* scales;
-  uint32_t scale_row;  // bytes from a row
-  size_t scale_stage;  // and from a stage to the next
-  Walk walk;
-  int stride;  // of the walk
   uint32_t lds;
   int lane, wave;
+  int D;               // stages of an item
+  bool odd;            // an odd number of steps
+  bool clip_scales;    // the activation scales lie by row
+  size_t scale_stage;  // bytes from a stage's to the next one's
+
+  // the kernel's arguments, read where this is called
+  __device__ __forceinline__ const claunch* launch() const {
+    const claunch* g = (const claunch*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(g));
+    return g;
+  }
 };
 
 // LDS-DMA: lane l's 16 (4) bytes at base + off go to LDS address lds + 16 l
@@ -247,51 +289,76 @@ __device__ __forceinline__ int scale_row(int n, int wave, int lane) {
   return 32 * (first_sub(n, wave >> 1) + ((at >> 1) & 1)) + (at >> 2);
 }
 
-// Row index DMA of item p (if there is one) into the index buffer: each wave
-// loads, and later reads, the indices of the 32 rows whose pieces it moves.
-__device__ __forceinline__ void fetch_rows(const Ctx& c, int p) {
-  if (!c.a.rows || p >= c.walk.hi) return;
-  int tt, tn;
-  walk_item(c.walk, p, tt, tn);
-  const Tile t = get_tile(c.a, c.ws, tt, c.walk.ntt);
-  dma4(wave_ptr(reinterpret_cast<const uint8_t*>(c.a.rows + t.row0)),
-       4u * (uint32_t)min(32 * c.wave + (c.lane & 31), t.n - 1), wave_u32(c.lds + kIdx + 256u * (uint32_t)c.wave));
+typedef __attribute__((address_space(3))) v4u lds_words;
+__device__ __forceinline__ Walk load_walk(const Ctx& c) {
+  const lds_words* p = reinterpret_cast<const lds_words*>((uintptr_t)(c.lds + kState + 64u * (uint32_t)c.wave));
+  v4u w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = p[i];
+  Walk k;
+  int* f = reinterpret_cast<int*>(&k);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = (int)wave_u32(w[i >> 2][i & 3]);
+  return k;
+}
+__device__ __forceinline__ void store_walk(const Ctx& c, const Walk& k) {
+  lds_words* p = reinterpret_cast<lds_words*>((uintptr_t)(c.lds + kState + 64u * (uint32_t)c.wave));
+  const int* f = reinterpret_cast<const int*>(&k);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    p[i] = v4u{(uint32_t)f[4 * i], (uint32_t)f[4 * i + 1], (uint32_t)f[4 * i + 2], (uint32_t)f[4 * i + 3]};
+}
+
+// Row index DMA of the walk's item into the index buffer: each wave loads, and
+// later reads, the indices of the 32 rows whose pieces it moves.
+__device__ __forceinline__ void fetch_rows(const Ctx& c, const Walk& k) {
+  const int32_t* xrows = c.launch()->xrows;
+  if (!xrows || !k.more) return;
+  dma4(reinterpret_cast<const uint8_t*>(xrows + k.row0), 4u * (uint32_t)min(32 * c.wave + (c.lane & 31), k.n - 1),
+       c.lds + kIdx + 256u * (uint32_t)c.wave);
 }
 
 // The last stage of an odd number of steps has no second step.  Its weights are
 // zeros; for the rows, what would lie past their end reads the first step's
 // bytes (a block that is NaN there is NaN in the first step too).
 __device__ __forceinline__ void clip_tail(const Ctx& c, Cursor& k) {
-  if (k.left != 1 || !(c.L.J & 1)) return;
+  if (k.left != 1 || !c.odd) return;
 #pragma unroll
   for (int u = 0; u < 4; ++u) k.a[u] -= (((uint32_t)c.lane & 7) ^ (uint32_t)((c.lane >> 4) + 4 * (u & 1))) & 4 ? 64u : 0u;
-  if (!c.a.offsets) k.sa -= 4u * (uint32_t)(c.lane & 1);
+  if (c.clip_scales) k.sa -= 4u * (uint32_t)(c.lane & 1);
 }
 
-// Points the cursor at item p (whose row indices are in the index buffer).
-__device__ __forceinline__ void enter(const Ctx& c, Cursor& k, int p) {
-  int tt, tn;
-  walk_item(c.walk, p, tt, tn);
-  const Tile t = get_tile(c.a, c.ws, tt, c.walk.ntt);
-  const Mx4Layout& L = c.L;
+// Moves the cursor to the walk's item (whose row indices are in the index
+// buffer), notes it for the wave's own use when it gets there, and the walk to
+// the one after it.
+__device__ __forceinline__ void enter(const Ctx& c, Cursor& k, Walk& walk) {
+  const claunch* g = c.launch();
+  const int tn = walk.base + walk.off;
+  const size_t J2 = (size_t)c.D * 2048;  // half the bytes of a weight tile
+  *reinterpret_cast<lds_words*>((uintptr_t)(c.lds + kInfo + 128u * (uint32_t)c.wave + 16u * (uint32_t)(walk.count & 7))) =
+      v4u{(uint32_t)walk.row0, (uint32_t)walk.n, (uint32_t)tn, 0u};
+  const uint32_t row_bytes = (uint32_t)g->L.K / 2;
+  const bool gather = g->xrows != nullptr;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int r = 8 * u + (c.lane >> 3);
     // logical piece of the lane: physical piece l % 8 of a row whose r / 2 % 8 is l / 16 + 4 (u % 2)
     const uint32_t piece = ((uint32_t)c.lane & 7) ^ (uint32_t)((c.lane >> 4) + 4 * (u & 1));
-    int x = t.row0 + min(32 * c.wave + r, t.n - 1);  // rows past the tile read its last one
-    if (c.a.rows) x = (int)((uint32_t)lds_i32(c.lds + kIdx + 4 * (64 * c.wave + r)) / (uint32_t)c.a.div);
-    k.a[u] = (uint32_t)max(min(x, c.a.X - 1), 0) * ((uint32_t)L.K / 2) + 16u * piece;
+    // rows past the tile read its last one
+    const int x = gather ? lds_i32(c.lds + kIdx + 4 * (64 * c.wave + r)) : walk.row0 + min(32 * c.wave + r, walk.n - 1);
+    k.a[u] = (uint32_t)x * row_bytes + 16u * piece;
   }
-  k.sa = (uint32_t)min(scale_row(t.n, c.wave, c.lane), t.n - 1) * c.scale_row + 4u * (uint32_t)(c.lane & 1);
-  k.x = wave_ptr(c.a.xq);
-  k.xs = wave_ptr(c.scales + (size_t)t.row0 * c.scale_row);
+  k.sa = (uint32_t)min(scale_row(walk.n, c.wave, c.lane), walk.n - 1) * (uint32_t)g->scale_row +
+         4u * (uint32_t)(c.lane & 1);
+  k.x = wave_ptr(g->a.xq);
+  k.xs = wave_ptr(g->scales + (size_t)walk.row0 * g->scale_row);
   // tiles past the last one read the last one; their columns are not stored
-  k.w = wave_ptr(c.a.packed + L.tile_off(t.e, min(tn * kBT + c.wave, L.NT - 1)));
-  k.ws = wave_ptr(c.a.packed + L.scale_off(t.e, min(2 * tn + (c.wave >> 2), L.NG - 1)) + 256 * (c.wave & 3));
-  k.p = p;
-  k.left = L.D;
+  const int nt = min(tn * kBT + c.wave, g->L.NT - 1), q = min(2 * tn + (c.wave >> 2), g->L.NG - 1);
+  k.w = wave_ptr(g->a.packed + ((size_t)walk.e * g->L.NT + nt) * (2 * J2));
+  k.ws = wave_ptr(g->a.packed + g->L.s_off + ((size_t)walk.e * g->L.NG + q) * (J2 / 2) + 256 * (c.wave & 3));
+  k.left = c.D;
   clip_tail(c, k);
+  next_item(g, walk);
 }
 
 // Load u (< 10) of the wave's share of the cursor's stage into the one at S, in
@@ -317,6 +384,8 @@ __device__ __forceinline__ void issue(const Ctx& c, const Cursor& k, uint32_t S,
 // last item its last stage is loaded again and never used).
 __device__ __forceinline__ void advance(const Ctx& c, Cursor& k) {
   if (k.left > 1) {
+    // a stage after the item was entered, when its successor's tile is known
+    if (k.left == c.D) fetch_rows(c, load_walk(c));
     --k.left;
     k.x += 128;
     k.w += 4096;
@@ -325,14 +394,17 @@ __device__ __forceinline__ void advance(const Ctx& c, Cursor& k) {
     clip_tail(c, k);
     return;
   }
-  const int p = k.p + c.stride;
-  if (p >= c.walk.hi) return;
-  // the indices were loaded when the cursor entered this item; with three
-  // stages or more since then the waits of the steps have covered them
-  if (c.a.rows && c.L.D < 3) wait_vmcnt<0>();
-  enter(c, k, p);
+  Walk walk = load_walk(c);
+  if (!walk.more) return;
+  // the indices were loaded a stage after the cursor entered this item; with
+  // four stages or more since then the waits of the steps have covered them
+  if (c.D < 5) {
+    if (c.D == 1) fetch_rows(c, walk);
+    wait_vmcnt<0>();
+  }
+  enter(c, k, walk);
+  store_walk(c, walk);
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the indices are read before they are replaced
-  fetch_rows(c, p + c.stride);
 }
 
 struct Addr {  // per lane, relative to a stage
@@ -370,11 +442,15 @@ __device__ __forceinline__ void shift_scales(Scales& s, const Addr& ad, const v4
   }
 }
 
-// MFMA m of K-half kHalf of step H: sub-tile m / 4, tile m % 4 (whose scale is
+// MFMA m (an item's first ones, kInit, add to zero) of K-half kHalf of step H: sub-tile m / 4, tile m % 4 (whose scale is
 // byte 2 (m % 2) + kHalf of its pair's dword).
-template <int H, int kHalf>
+template <int H, int kHalf, bool kInit>
 __device__ __forceinline__ void multiply(v16f (&acc)[2][4], const Frag& f, const Scales& s, int m) {
   const int i = m >> 2, t = m & 3;
+  if constexpr (kInit) {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[i][t][v] = 0.0f;
+  }
   if (t & 1)
     mfma<kHalf, 2 + kHalf>(acc[i][t], f.x[i], f.w[t], s.x[i][H], s.w[2 * H + (t >> 1)]);
   else
@@ -387,7 +463,7 @@ __device__ __forceinline__ void multiply(v16f (&acc)[2][4], const Frag& f, const
 // this one is; in step 0 its first step's weights (whose place is free behind
 // the barrier), in step 1 the row pieces and, in the next stage's step 0, the
 // rest, spread over the MFMAs.
-template <int S, int H>
+template <int S, int H, bool kInit>
 __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, uint32_t cur, uint32_t nxt,
                                      v16f (&acc)[2][4], Frag& f0, Frag& f1, Scales& s) {
   constexpr int M = 4 * S;  // MFMAs of a half
@@ -397,7 +473,7 @@ __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, ui
     const uint32_t xa = cur + ad.a[2 * H + 1], wa = cur + ad.w + (uint32_t)(H * kW + 1024);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      multiply<H, 0>(acc, f0, s, m);
+      multiply<H, 0, kInit>(acc, f0, s, m);
 #pragma unroll
       for (int q = 0; q < R; ++q)
         if (q * M / R == m) read_frag(f1, xa, wa, q);
@@ -431,7 +507,7 @@ __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, ui
     Scales ns;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      multiply<H, 1>(acc, f1, s, m);
+      multiply<H, 1, false>(acc, f1, s, m);
       if (m == 0) {
         publish();
         if constexpr (H == 1) read_scales<S>(ns, nxt, ad, raw);
@@ -519,7 +595,7 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
   v16f acc[2][4];
   Frag f0, f1;
   Scales s;
-  uint32_t cur = wave_u32(c.lds + (uint32_t)(stage * kStage)), nxt;
+  uint32_t cur = wave_u32(c.lds + (uint32_t)(stage * kStage)), nxt = wave_u32(c.lds + (uint32_t)((stage ^ 1) * kStage));
   if constexpr (S > 0) {
 #pragma unroll
     for (int i = 0; i < S; ++i)
@@ -533,23 +609,24 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
     for (int q = 0; q < S + 4; ++q) read_frag(f0, cur + ad.a[0], cur + ad.w, q);
     shift_scales<S>(s, ad, raw);
   }
-  for (int d = 0; d < c.L.D; ++d) {
+  for (int d = 0; d < c.D; ++d) {
     cur = wave_u32(c.lds + (uint32_t)(stage * kStage));
     nxt = wave_u32(c.lds + (uint32_t)((stage ^ 1) * kStage));
-    step<S, 0>(c, k, ad, cur, nxt, acc, f0, f1, s);
-    step<S, 1>(c, k, ad, cur, nxt, acc, f0, f1, s);
+    step<S, 0, false>(c, k, ad, cur, nxt, acc, f0, f1, s);
+    step<S, 1, false>(c, k, ad, cur, nxt, acc, f0, f1, s);
     stage ^= 1;
   }
   if constexpr (S > 0) {
     constexpr int kO = kGlu ? 2 : 4;
     constexpr uint32_t kB = kF32 ? 4 : 2;
-    const int g = c.lane >> 5, left = c.L.N / 32 - kO * group, f = min(left, kO);
-    const size_t row_bytes = (size_t)c.L.N * kB;
-    const uint32_t off = ((uint32_t)(4 * g) * (uint32_t)c.L.N + (uint32_t)f * (uint32_t)(c.lane & 31)) * kB;
+    const claunch* launch = c.launch();
+    const int N = launch->L.N, g = c.lane >> 5, f = min(N / 32 - kO * group, kO);
+    const size_t row_bytes = (size_t)N * kB;
+    const uint32_t off = ((uint32_t)(4 * g) * (uint32_t)N + (uint32_t)f * (uint32_t)(c.lane & 31)) * kB;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const int m = 32 * (sub0 + i);
-      uint8_t* base = static_cast<uint8_t*>(c.a.y) + ((size_t)(t.row0 + m) * c.L.N + (size_t)(32 * kO) * group) * kB;
+      uint8_t* base = static_cast<uint8_t*>(launch->a.y) + ((size_t)(t.row0 + m) * N + (size_t)(32 * kO) * group) * kB;
       gbyte* gb = reinterpret_cast<gbyte*>(reinterpret_cast<uintptr_t>(wave_ptr(base)));
       if (f == kO && m + 32 <= t.n)
         store_sub<kGlu, kF32, false>(acc[i], gb, row_bytes, off, 32, f);
@@ -561,28 +638,38 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
 
 template <bool kGlu, bool kF32>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void tiled_kernel(
-    Mx4Args a, Mx4Layout L, const int32_t* ws, const uint8_t* scales, int dense_tiles) {
+    Launch launch) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  Ctx c{a, L, ws, scales ? scales : a.xs, scales ? 8u : (uint32_t)L.K / 32, scales ? 8 * (size_t)a.P : 8, {},
-        (int)(gridDim.x >> 3), (uint32_t)(uintptr_t)(lds_u8*)lds, lane, wave};
-  c.walk.ntt = a.offsets ? *reinterpret_cast<const cint*>(reinterpret_cast<uintptr_t>(ws)) : dense_tiles;
-  c.walk.ntn = (L.NT + kBT - 1) / kBT;
-  const int items = c.walk.ntt * c.walk.ntn, per = (items + 7) / 8;
-  // workgroup b runs on XCD b % 8, which owns the run [x per, x per + per)
-  c.walk.lo = min((int)(blockIdx.x & 7) * per, items);
-  c.walk.hi = min(c.walk.lo + per, items);
-  const int first = c.walk.lo + (int)(blockIdx.x >> 3);
-  if (first >= c.walk.hi) return;  // uniform: before any barrier
-
+  const Ctx c{(uint32_t)(uintptr_t)(lds_u8*)lds, lane, wave, launch.L.D, (launch.L.J & 1) != 0, !launch.a.offsets,
+              launch.scale_stage};
   Cursor k;
-  fetch_rows(c, first);
-  wait_vmcnt<0>();
-  enter(c, k, first);
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  fetch_rows(c, first + c.stride);
+  int mine;  // items of this workgroup
+  {
+    const claunch* g = c.launch();
+    Walk walk;
+    walk.ntt = g->a.offsets ? *reinterpret_cast<const cint*>(reinterpret_cast<uintptr_t>(g->ws)) : g->tiles;
+    walk.ntn = (g->L.NT + kBT - 1) / kBT;
+    const int items = walk.ntt * walk.ntn, per = (items + 7) / 8;
+    // workgroup b runs on XCD b % 8, which owns the run [x per, x per + per)
+    const int lo = min((int)(blockIdx.x & 7) * per, items);
+    walk.hi = min(lo + per, items);
+    walk.stride = (int)(gridDim.x >> 3);
+    walk.p = lo + (int)(blockIdx.x >> 3);
+    if (walk.p >= walk.hi) return;  // uniform: before any barrier
+    mine = (walk.hi - walk.p + walk.stride - 1) / walk.stride;
+    walk.count = 0;
+    walk.more = 1;
+    locate(walk);
+    look_up(g, walk);
+    fetch_rows(c, walk);
+    wait_vmcnt<0>();
+    enter(c, k, walk);
+    store_walk(c, walk);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
   const uint32_t s0 = wave_u32(c.lds), s1 = wave_u32(c.lds + (uint32_t)kStage);
 #pragma unroll
   for (int u = 0; u < 10; ++u) issue(c, k, s0, u);
@@ -600,10 +687,11 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
   ad.sw = opaque((uint32_t)(kOffSW + 1024 * wn + 16 * lane));
   ad.shift = (uint32_t)(16 * g);
   int stage = 0;
-  for (int p = first; p < c.walk.hi; p += c.stride) {
-    int tt, tn;
-    walk_item(c.walk, p, tt, tn);
-    const Tile t = get_tile(a, ws, tt, c.walk.ntt);
+  for (int i = 0; i < mine; ++i) {
+    // as the cursor noted it
+    const v4u info = lds_v4(c.lds + kInfo + 128 * wave + 16 * (i & 7));
+    const Tile t{0, (int)wave_u32(info.x), (int)wave_u32(info.y)};
+    const int tn = (int)wave_u32(info.z);
     const int sub0 = first_sub(t.n, wm), live = sub_tiles(t.n, wm);
     const uint32_t row = (uint32_t)(32 * sub0 + r);
 #pragma unroll
@@ -638,28 +726,35 @@ int workgroups() {
 size_t mx4_tiled_ws_bytes(long P, int E, int K) { return scales_at(P, E) + 8 * (size_t)P * ((K + 255) / 256); }
 
 hipError_t launch_mx4_tiled(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, void* ws, hipStream_t st) {
-  int32_t* list = static_cast<int32_t*>(ws);
-  uint8_t* scales = nullptr;
+  Launch g{a, L, nullptr, nullptr, a.xs, 8, L.K / 32, (a.P + kBM - 1) / kBM, 0};
   if (a.offsets) {
-    scales = static_cast<uint8_t*>(ws) + scales_at(a.P, L.E);
+    int32_t* list = static_cast<int32_t*>(ws);
+    int32_t* xrows = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + rows_at(a.P, L.E));
+    uint8_t* scales = static_cast<uint8_t*>(ws) + scales_at(a.P, L.E);
     const size_t threads = (size_t)a.P * ((L.D + kPer - 1) / kPer);
     hipLaunchKernelGGL(tiles_kernel, dim3((unsigned)(1 + (threads + 1023) / 1024)), dim3(1024), 0, st, a, L.E, L.K,
-                       (int)tile_cap(a.P, L.E), list, scales);
+                       (int)tile_cap(a.P, L.E), list, xrows, scales);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    g.ws = list;
+    g.xrows = a.rows ? xrows : nullptr;
+    g.scales = scales;
+    g.scale_stage = 8 * (size_t)a.P;
+    g.scale_row = 8;
+  } else {
+    g.height = tile_height(a.P, g.tiles);
   }
-  const int dense_tiles = (a.P + kBM - 1) / kBM;
   const dim3 grid((unsigned)workgroups()), block(64 * kWaves);
   if (L.glu) {
     if (fp32_out)
-      hipLaunchKernelGGL((tiled_kernel<true, true>), grid, block, 0, st, a, L, list, scales, dense_tiles);
+      hipLaunchKernelGGL((tiled_kernel<true, true>), grid, block, 0, st, g);
     else
-      hipLaunchKernelGGL((tiled_kernel<true, false>), grid, block, 0, st, a, L, list, scales, dense_tiles);
+      hipLaunchKernelGGL((tiled_kernel<true, false>), grid, block, 0, st, g);
   } else {
     if (fp32_out)
-      hipLaunchKernelGGL((tiled_kernel<false, true>), grid, block, 0, st, a, L, list, scales, dense_tiles);
+      hipLaunchKernelGGL((tiled_kernel<false, true>), grid, block, 0, st, g);
     else
-      hipLaunchKernelGGL((tiled_kernel<false, false>), grid, block, 0, st, a, L, list, scales, dense_tiles);
+      hipLaunchKernelGGL((tiled_kernel<false, false>), grid, block, 0, st, g);
   }
   return hipGetLastError();
 }
