@@ -31,7 +31,8 @@ def _round_to(table, a):
 
 def quant(v, fmt):
     """[M, K] values -> (codes, scale codes): packed nibbles [M, K/2] for "mxfp4", bytes [M, K] for "mxfp8"."""
-    v = np.asarray(v, dtype=np.float64)
+    with np.errstate(invalid="ignore"):  # signalling NaNs become quiet ones
+        v = np.asarray(v, dtype=np.float64)
     M, K = v.shape
     b = v.reshape(M, K // 32, 32)
     amax = np.abs(b).max(-1)
