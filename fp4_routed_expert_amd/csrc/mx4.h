@@ -21,8 +21,8 @@ enum class ElemType : int { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
 // elements of one scale), so that a lane's two blocks are neighbours: a token
 // row's 64 bytes of a step are read as two 16-byte pieces at 32 g, and its
 // two scale bytes as one 16-bit word.  (Which K a lane holds is free as long
-// as both operands agree.)  A tile's K-steps are consecutive; an odd number of them is followed by one of
-// zeros.
+// as both operands agree.)  A tile's K-steps are consecutive; an odd number of
+// them is followed by one of zeros.
 //
 // Columns: tiles come in groups of four, which one wave of the tiled kernel
 // multiplies.  The f tiles of a group (f = 4, fewer in the last) interleave
@@ -69,6 +69,13 @@ __device__ __forceinline__ v16f mfma_fp4(v4u a, v4u b, v16f c, uint32_t sa, uint
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
       __builtin_shufflevector(ai, ai, 0, 1, 2, 3, -1, -1, -1, -1),
       __builtin_shufflevector(bi, bi, 0, 1, 2, 3, -1, -1, -1, -1), c, 4, 4, kA, (int)sa, kB, (int)sb);
+}
+
+// SiLU(g) u.  The exponential comes straight from the exp2 instruction, whose
+// results below 2^-126 are 0 here, as 1 + them is 1 anyway; SiLU first, so that
+// a product g u past fp32's range does not meet a sigmoid of zero.
+__device__ __forceinline__ float glu_out(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
 }
 
 // ------------------------------------------------------------------- MXFP4

@@ -18,14 +18,15 @@ bool norm_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_FP32; }
 constexpr int kMaxMx4E = 1024;
 constexpr int kMaxNormH = 16384;
 
-// A grid of one workgroup per 1024 groups of eight elements has to fit 2^31.
-bool too_many(int32_t M, int32_t K) { return (int64_t)M * K / 8192 >= ((int64_t)1 << 31) - 1; }
+// A grid of one workgroup of 256 threads per 1024 groups of eight elements has
+// to stay below 2^32 threads.
+bool too_many(int32_t M, int32_t K) { return (int64_t)M * K / 8192 >= ((int64_t)1 << 24) - 1; }
 
 moe_status_t check_enk(int32_t E, int32_t N, int32_t K, int32_t glu) {
   if (E < 1 || N < 1 || K < 1 || (glu != 0 && glu != 1)) return MOE_ERR_INVALID_ARGUMENT;
   if (E > kMaxMx4E || N % 32 != 0 || K % 128 != 0 || N > (1 << 20) || K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
-  // packing runs one thread per 16 bytes
-  if (Mx4Layout(E, N, K, glu).s_off / 16 / 256 >= ((size_t)1 << 31) - 1) return MOE_ERR_UNSUPPORTED;
+  // packing runs a grid of up to 2^20 x 65535 workgroups of 4 KiB
+  if (Mx4Layout(E, N, K, glu).s_off / 4096 > (size_t)65535 << 20) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -38,8 +39,7 @@ moe_status_t check_mx4_weights(const moe_mxfp4_weights_t* w) {
   return MOE_OK;
 }
 
-// The tiled product addresses activation rows by 32-bit byte offsets, up to
-// 4 KiB of which the instructions' own offsets take.
+// The tiled product addresses activation rows by 32-bit byte offsets.
 bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K / 2 > ((int64_t)1 << 32) - 4096; }
 
 // 0: stream the weights, 1: tiled, -1: bad flags.  By default the weights are

@@ -18,11 +18,13 @@ namespace moe {
 namespace {
 
 // ------------------------------------------------------------------- packing
-// One thread per 16 bytes of a tile: piece i of the packed weights.
+// One thread per 16 bytes of a tile: piece i of the packed weights.  A launch
+// dimension holds fewer than 2^32 threads, so larger weights run in y too.
+constexpr size_t kPackX = 1 << 20;
 __global__ __launch_bounds__(256) void pack_kernel(const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws,
                                                    const uint8_t* __restrict__ uq, const uint8_t* __restrict__ us,
                                                    Mx4Layout L, uint8_t* __restrict__ packed) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const size_t i = (blockIdx.y * kPackX + blockIdx.x) * 256 + threadIdx.x;
   const size_t n = (size_t)L.E * L.NT * L.D * 256;
   if (i >= n) return;
   const int lane = (int)(i & 63), s = (int)(i >> 6) & 1;
@@ -152,7 +154,7 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(Mx4Args a, Mx4Layout L)
 #pragma unroll
         for (int w = 1; w < NW; ++w) up += red[w][4 + b][lane];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) s[v] = silu_mul(s[v], up[v]);
+        for (int v = 0; v < 4; ++v) s[v] = glu_out(s[v], up[v]);
       }
       if (nt0 + t >= L.NT) continue;
       const int col = L.column(nt0 + t, n);
@@ -184,8 +186,9 @@ void stream_as(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, hipStream_t 
 
 hipError_t launch_mx4_pack(const uint8_t* wq, const uint8_t* ws, const uint8_t* uq, const uint8_t* us,
                            const Mx4Layout& L, uint8_t* packed, hipStream_t st) {
-  const size_t n = (size_t)L.E * L.NT * L.D * 256;
-  hipLaunchKernelGGL(pack_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, wq, ws, uq, us, L, packed);
+  const size_t n = (size_t)L.E * L.NT * L.D;  // workgroups
+  const dim3 grid((unsigned)(n < kPackX ? n : kPackX), (unsigned)((n + kPackX - 1) / kPackX));
+  hipLaunchKernelGGL(pack_kernel, grid, dim3(256), 0, st, wq, ws, uq, us, L, packed);
   return hipGetLastError();
 }
 

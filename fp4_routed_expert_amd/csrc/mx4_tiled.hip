@@ -372,7 +372,7 @@ __device__ __forceinline__ void issue(const Ctx& c, const Cursor& k, uint32_t S,
     case 2: dma16(k.x, k.a[0], S + 4096u * w); break;
     case 3: dma16(k.x, k.a[1], S + 4096u * w + 1024u); break;
     case 4: dma16(k.x, k.a[2], S + 4096u * w + 2048u); break;
-    case 5: dma16(k.x, k.a[3], S + 4096u * w + 3072u); break;
+    case 5: dma16(k.x, k.a[3], S + 4096u * w + 3u * 1024u); break;
     case 6: dma4(k.xs, k.sa, S + (uint32_t)kOffSA + 256u * w); break;
     case 7: dma4(k.ws, 4u * (uint32_t)c.lane, S + (uint32_t)kOffSW + 256u * w); break;
     case 8: dma16(k.w + 2048, l16, S + (uint32_t)(kOffW + kW) + 2048u * w); break;
@@ -528,13 +528,6 @@ __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, ui
 #pragma unroll
     for (int u = kFrom; u < kTo; ++u) issue(c, k, cur, u);
   }
-}
-
-// SiLU(g) u for the SwiGLU epilogue, as silu_mul but with the exponential
-// straight from the exp2 instruction (whose results below 2^-126 are 0 here,
-// as 1 + them is 1 anyway).
-__device__ __forceinline__ float glu_out(float g, float u) {
-  return g * u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
 // Global (not flat) pointers: flat stores would count as LDS traffic too.

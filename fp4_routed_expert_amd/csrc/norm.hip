@@ -158,12 +158,15 @@ __device__ __forceinline__ void finish8(const NormArgs& a, size_t row, int h, co
 }
 
 // One row per workgroup of NW waves, kC groups of eight columns per thread
-// (H <= 512 NW kC, H % 8 == 0).
+// (H <= 512 NW kC, H % 8 == 0).  A launch dimension holds fewer than 2^32
+// threads, so more rows than kRowsX run in y too.
+constexpr unsigned kRowsX = 1 << 16;
 template <int NW, int kC>
 __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
   __shared__ double part[2][NW];
   const int H = a.H;
-  const size_t t = blockIdx.x, row = t * H;
+  const size_t t = blockIdx.y * kRowsX + blockIdx.x, row = t * H;
+  if (t >= (size_t)a.T) return;
   float v[kC][8];
   const bool after = a.res != nullptr;
   float res[kC][8];
@@ -218,7 +221,9 @@ __global__ __launch_bounds__(64 * NW) void norm_kernel(NormArgs a) {
 
 template <int NW, int kC>
 void norm_as(const NormArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((norm_kernel<NW, kC>), dim3((unsigned)a.T), dim3(64 * NW), 0, st, a);
+  const unsigned T = (unsigned)a.T;
+  const dim3 grid(T < kRowsX ? T : kRowsX, (T + kRowsX - 1) / kRowsX);
+  hipLaunchKernelGGL((norm_kernel<NW, kC>), grid, dim3(64 * NW), 0, st, a);
 }
 
 }  // namespace

@@ -90,6 +90,8 @@ def dequant_mx(q: torch.Tensor, s: torch.Tensor, format: str, dtype: torch.dtype
     -> [M, K] of ``dtype``."""
     if format not in ("mxfp4", "mxfp8"):
         raise ValueError(f"format {format!r}")
+    if s.dim() != 2:
+        raise ValueError(f"s: shape {tuple(s.shape)}, not [M, K/32]")
     M, K = s.shape[0], s.shape[1] * 32
     dev = q.device
     if out is None:

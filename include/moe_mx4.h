@@ -112,7 +112,8 @@ moe_status_t moe_mxfp4_dense_forward(const moe_mxfp4_weights_t* w /*(host), E ==
  *     offsets past P and rows past X are read as the last row's, never beyond.
  *   y [P, N] of y_type (16-byte aligned), rows in expert order
  *   workspace >= moe_mxfp4_grouped_workspace_size(P, E, N, K, glu) bytes,
- *     256-byte aligned; contents ignored on entry
+ *     256-byte aligned; contents ignored on entry.  Calls (or captured graphs)
+ *     that may overlap need one each.
  *   flags as above; X * K <= 2^33 - 8192
  */
 size_t moe_mxfp4_grouped_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K, int32_t glu);

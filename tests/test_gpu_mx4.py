@@ -197,6 +197,25 @@ def test_dense_glu(dev):
                 check(y, *ref.glu(x, w, u, out), f"T {T} K {K} N {N} {out} {flags}")
 
 
+@pytest.mark.parametrize("flags", [DECODE, PREFILL])
+def test_dense_glu_far_gates(dev, flags):
+    """Gate and up sums of 2^100 (their product is past fp32's range): a closed gate gives zero, an open one
+    its product.  Each sum is one product of powers of two, so the outputs are exact."""
+    K, N, T = 128, 32, 40
+    xq, xs = np.zeros((T, K // 2), np.uint8), np.full((T, K // 32), 127, np.uint8)
+    xq[:, 0] = 2                                                            # element 0: 1.0
+    wq, uq = np.zeros((N, K // 2), np.uint8), np.zeros((N, K // 2), np.uint8)
+    ws, us = np.full((N, K // 32), 227, np.uint8), np.full((N, K // 32), 227, np.uint8)
+    wq[:, 0], uq[:, 0] = 10, 2                                              # -2^100, 2^100
+    uq[1::3, 0] = 10                                                        # -2^100, -2^100
+    wq[2::3, 0], us[2::3] = 2, 27                                           # 2^100, 2^-100
+    pw = moe.mxfp4_prepack_glu(*(dev_t(a, dev) for a in (wq, ws, uq, us)))
+    want = np.where(np.arange(N) % 3 == 2, 1.0, 0.0)
+    for out in ("bf16", "fp32"):
+        y = host(moe.mxfp4_dense(pw, dev_t(xq, dev), dev_t(xs, dev), DT[out], flags))
+        assert (y == want).all()
+
+
 def group_case(dev, sizes, K, N, glu=False, gather=None, out="bf16", flags=0, lead=0, tail=0, seed=0):
     """Groups of the given sizes in rows [lead, lead + sum) of P = lead + sum + tail; gather: (X, div)."""
     r = rng(len(sizes), K, N, seed)
@@ -288,6 +307,67 @@ def test_products_repeat_their_bits(dev):
         for _ in range(5):
             torch.randn(1 << 20, device=dev).sort()
             assert torch.equal(first, moe.mxfp4_grouped(pw, dev_t(xq, dev), dev_t(xs, dev), off, flags=flags))
+
+
+def some_rows(dev, y, x_of, w_of, rows, out="bf16"):
+    for e, i in rows:
+        w = w_of(e)
+        want, err = ref.product(x_of(i), w, out)
+        check(y[i:i + 1], want, err, f"row {i}")
+
+
+@pytest.mark.parametrize("flags", [DECODE, PREFILL])
+def test_grouped_offsets_past_32_bits(dev, flags):
+    """Weights, activations and outputs of more than 4 GiB each: the last rows and experts."""
+    g = torch.Generator(device=dev).manual_seed(3)
+    # 4.3 GiB of weights: 70 experts of 16384 x 7680 codes
+    E, N, K = 70, 16384, 7680
+    wq = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device=dev, generator=g)
+    ws = torch.randint(118, 122, (E, N, K // 32), dtype=torch.uint8, device=dev, generator=g)
+    pw = moe.mxfp4_prepack(wq, ws)
+    assert pw.buffer.numel() > 1 << 32
+    r = rng(29)
+    xq, xs, x = rows4(r, 40, K)
+    off = np.zeros(E + 1, np.int32)
+    off[1:-1], off[-1] = 3, 40                                              # expert 0: 3 rows, the last one: 37
+    y = moe.mxfp4_grouped(pw, dev_t(xq, dev), dev_t(xs, dev), dev_t(off, dev), flags=flags)
+    some_rows(dev, y, lambda i: x[i:i + 1], lambda e: ref.values(host(wq[e]), host(ws[e])), [(0, 2), (E - 1, 3), (E - 1, 39)])
+    del wq, ws, pw, y
+    # 4.5 GiB of outputs, and activation rows up to the largest byte offset
+    N, K = 7168, 256
+    P, X = 340000, ((1 << 33) - 8192) // K
+    xq = torch.empty(X, K // 2, dtype=torch.uint8, device=dev).random_(0, 256, generator=g)
+    xs = torch.randint(120, 124, (X, K // 32), dtype=torch.uint8, device=dev, generator=g)
+    wq, ws, w = weights4(r, 2, N, K)
+    rows = torch.arange(X - P, X, dtype=torch.int32, device=dev)
+    off = torch.tensor([0, 5, P], dtype=torch.int32, device=dev)
+    y = moe.mxfp4_grouped(moe.mxfp4_prepack(dev_t(wq, dev), dev_t(ws, dev)), xq, xs, off, rows=rows, flags=flags)
+    assert y.numel() * 2 > 1 << 32
+    some_rows(dev, y, lambda i: ref.values(host(xq[X - P + i:X - P + i + 1]), host(xs[X - P + i:X - P + i + 1])), lambda e: w[e],
+              [(0, 0), (0, 4), (1, 5), (1, 200000), (1, P - 1)])
+    with pytest.raises(moe.MoeError):                                       # one row more
+        moe.mxfp4_grouped(moe.mxfp4_prepack(dev_t(wq, dev), dev_t(ws, dev)), xq.new_empty(X + 1, K // 2),
+                          xs.new_empty(X + 1, K // 32), off, rows=rows)
+
+
+def test_quant_and_norm_past_32_bits(dev):
+    """More than 2^32 bytes of rows: the last ones."""
+    g = torch.Generator(device=dev).manual_seed(5)
+    M, K = 300000, 8192
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+    x.normal_(generator=g)
+    q, s = moe.quant_mxfp4(x)
+    v = moe.dequant_mx(q, s, "mxfp4")
+    z, q8, s8 = moe.norm_before(x, torch.ones(K, device=dev), quant="mxfp8")
+    for i in (0, 150000, M - 1):
+        a = host(x[i:i + 1])
+        qr, sr = ref.quant(a, "mxfp4")
+        assert np.array_equal(host(q[i:i + 1]), qr) and np.array_equal(host(s[i:i + 1]), sr)
+        assert np.array_equal(host(v[i:i + 1]), ref.values(qr, sr).astype(np.float32))
+        zr = ref.norm_before(a, np.ones(K, np.float32), 1e-6)
+        assert np.array_equal(host(z[i:i + 1]), zr)
+        qr, sr = ref.quant(zr, "mxfp8")
+        assert np.array_equal(host(q8[i:i + 1]), qr) and np.array_equal(host(s8[i:i + 1]), sr)
 
 
 # --------------------------------------------------------------------- norms
