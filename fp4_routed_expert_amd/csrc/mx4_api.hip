@@ -45,13 +45,12 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K / 2 > ((int64_
 // 0: stream the weights, 1: tiled, -1: bad flags.  By default the weights are
 // streamed while the groups average at most 16 rows (measured with 64 and 256
 // experts: at 12 rows streaming is 3-17 % faster, at 24 rows 5-24 % slower), or
-// while streaming makes at most 1536 passes of 32 rows over a weight tile, six
+// while streaming makes at most 1024 passes of 32 rows over a weight tile, four
 // per CU: the tiled product has few tiles then.  Dense, us, streaming against
-// tiled: K 4096, N 1536, 333 rows (528 passes) 12 and 20, 1024 rows (1536) 20
-// and 26; K 16384, N 7168, 128 rows (896) 56-63 and 79, 192 rows (1344) 88 and
-// 84; K 2048, N 7168, 192 rows (1344) 13 and 14, 256 rows (1792) 16 and 17, 384
-// rows (2688) 21 and 15; K 1536, N 4096, 768 rows (3072) 17 and 15.
-constexpr int64_t kStreamRows = 16, kStreamPasses = 1536;
+// tiled: K 4096, N 1536, 333 rows (528 passes) 12 and 16, 1024 rows (1536) 20
+// and 16; K 16384, N 7168, 128 rows (896) 63 and 70, 256 rows (1792) 119 and
+// 70; K 1536, N 4096, 256 rows (1024) 8.2 and 9.7, 512 rows (2048) 12 and 10.
+constexpr int64_t kStreamRows = 16, kStreamPasses = 1024;
 int choose_path(int64_t P, const Mx4Layout& L, bool grouped, uint32_t flags) {
   const bool fd = flags & MOE_FLAG_FORCE_DECODE, fp = flags & MOE_FLAG_FORCE_PREFILL;
   if ((flags & ~(MOE_FLAG_FORCE_DECODE | MOE_FLAG_FORCE_PREFILL)) != 0 || (fd && fp)) return -1;

@@ -148,9 +148,10 @@ def test_dense(dev, T, K, N, out, flags):
 
 
 @pytest.mark.parametrize("T,K,N,flags", [(8, 16384, 512, 0), (1, 7168, 2048, 0), (1100, 2048, 7168, PREFILL),
-                                         (2300, 512, 4096, PREFILL)])
+                                         (2300, 512, 4096, PREFILL), (2300, 384, 7168, 0), (4600, 256, 7168, 0),
+                                         (1024, 1024, 2048, 0), (1500, 2048, 1056, 0)])
 def test_dense_large(dev, T, K, N, flags):
-    """Long sums, and more work items than workgroups (each walks several)."""
+    """Long sums, tiles of every height, and more work items than workgroups (each walks several)."""
     dense_case(dev, T, K, N, "bf16", flags)
 
 
