@@ -16,6 +16,7 @@ bool known_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_FP16 || 
 bool norm_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_FP32; }
 
 constexpr int kMaxMx4E = 1024;
+constexpr int kMaxMx4P = INT32_MAX - 256;  // a tile past the last row still counts in 32 bits
 constexpr int kMaxNormH = 16384;
 
 // A grid of one workgroup of 256 threads per 1024 groups of eight elements has
@@ -50,14 +51,18 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K / 2 > ((int64_
 // tiled: K 4096, N 1536, 333 rows (528 passes) 12 and 16, 1024 rows (1536) 20
 // and 16; K 16384, N 7168, 128 rows (896) 63 and 70, 256 rows (1792) 119 and
 // 70; K 1536, N 4096, 256 rows (1024) 8.2 and 9.7, 512 rows (2048) 12 and 10.
-constexpr int64_t kStreamRows = 16, kStreamPasses = 1024;
+// Grouped, where the tiled product lists its tiles first, up to 1280 (a group's
+// last pass counted half): 16 experts, K 2048, N 512, 2000 rows (1120) 12 and
+// 21; 4 experts, K 2048, N 4096, 256 rows (1280) 11 and 15; 8 experts, K 16384,
+// N 2048, 400 rows (1024) 70 and 59, K 4096, N 4096, 512 rows (2560) 47 and 30.
+constexpr int64_t kStreamRows = 16, kStreamPasses = 1024, kStreamGroupedPasses = 1280;
 int choose_path(int64_t P, const Mx4Layout& L, bool grouped, uint32_t flags) {
   const bool fd = flags & MOE_FLAG_FORCE_DECODE, fp = flags & MOE_FLAG_FORCE_PREFILL;
   if ((flags & ~(MOE_FLAG_FORCE_DECODE | MOE_FLAG_FORCE_PREFILL)) != 0 || (fd && fp)) return -1;
   if (fd) return 0;
   if (fp) return 1;
-  const int64_t passes = grouped ? P / 32 + L.E : (P + 31) / 32;
-  return P <= kStreamRows * L.E || passes * L.NT <= kStreamPasses ? 0 : 1;
+  const int64_t passes = grouped ? P / 32 + (L.E + 1) / 2 : (P + 31) / 32;
+  return P <= kStreamRows * L.E || passes * L.NT <= (grouped ? kStreamGroupedPasses : kStreamPasses) ? 0 : 1;
 }
 
 moe_status_t run_product(const Mx4Args& a, const Mx4Layout& L, int path, int32_t y_type, void* ws, hipStream_t stream) {
@@ -164,7 +169,7 @@ moe_status_t moe_mxfp4_dense_forward(const moe_mxfp4_weights_t* w, const uint8_t
 }
 
 size_t moe_mxfp4_grouped_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K, int32_t glu) {
-  if (P < 0 || check_enk(E, N, K, glu) != MOE_OK) return 0;
+  if (P < 0 || P > kMaxMx4P || check_enk(E, N, K, glu) != MOE_OK) return 0;
   return PackedLayout::align256(mx4_tiled_ws_bytes(P, E, K));
 }
 
@@ -178,7 +183,7 @@ moe_status_t moe_mxfp4_grouped_forward(const moe_mxfp4_weights_t* w, const uint8
   const Mx4Layout L(w->E, w->N, w->K, w->glu != 0);
   const int path = choose_path(P, L, true, flags);
   if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
-  if (rows_too_large(X, w->K)) return MOE_ERR_UNSUPPORTED;
+  if (rows_too_large(X, w->K) || P > kMaxMx4P) return MOE_ERR_UNSUPPORTED;
   if (P == 0) return MOE_OK;
   if (X < 1 || (!rows && X < P)) return MOE_ERR_INVALID_ARGUMENT;
   if (!xq || !xs || !offsets || !y) return MOE_ERR_INVALID_ARGUMENT;

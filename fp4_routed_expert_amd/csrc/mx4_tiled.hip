@@ -60,7 +60,7 @@ constexpr int kState = kInfo + kWaves * 128; // and where its cursor goes next
 constexpr int kLds = kState + kWaves * 64;
 static_assert(kStage % 1024 == 0 && kLds <= 160 * 1024, "LDS");
 
-// One entry per 256 rows (at most) of a group, of equal heights.
+// A group's tiles of at most 256 rows are of equal heights.
 struct Tile {
   int e, row0, n;
 };
@@ -70,20 +70,31 @@ __host__ __device__ __forceinline__ int tile_height(int n, int tiles) {
   return ((n + 31) / 32 + tiles - 1) / tiles * 32;
 }
 
+// How long tiles x ntn items take whose rows are at most s sub-tiles per SIMD
+// (64 s rows): they run in rounds of one per CU, an item takes about 7 + 2 s
+// units (what does not shrink is the wait for its loads: K 7168, N 2048, 512
+// rows: 39 us with s = 4, 28 with 2, 23 with 1).  The s of the fewest units is
+// taken, the largest on a tie.  Dense, K 7168, N 2048, 1024 rows: 24 us against
+// 39 with tiles of 256 rows; K 4096, N 1536, 4604 rows: 25 against 29.
+__host__ __device__ __forceinline__ float item_units(uint32_t tiles, int ntn, float per_cu, int s) {
+  return ceilf((float)tiles * (float)ntn * per_cu) * (float)(7 + 2 * s);  // per_cu: 1 / CUs
+}
+
 // Workspace of a grouped product: the number of tiles, from byte 16 on four
 // words per tile, from rows_at() on the x row of each sorted row, and from
 // scales_at() on the activation scales by stage: the eight bytes of stage d of
 // sorted row p at 8 (d P + p), so that a tile's scales of a stage are one run
 // instead of a request to L2 for each row.
-long tile_cap(long P, int E) { return P / kBM + (P < E ? P : E); }
+long tile_cap(long P, int E) { return P / 64 + (P < E ? P : E); }
 size_t rows_at(long P, int E) { return PackedLayout::align256(16 + 16 * (size_t)tile_cap(P, E)); }
 size_t scales_at(long P, int E) { return PackedLayout::align256(rows_at(P, E) + 4 * (size_t)P); }
 
 // Block 0 lists the tiles, each thread of the others moves kPer stages of one
 // row's scales.
 constexpr int kPer = 8;
-__global__ __launch_bounds__(1024) void tiles_kernel(Mx4Args a, int E, int K, int cap, int32_t* __restrict__ ws,
-                                                     int32_t* __restrict__ xrows, uint8_t* __restrict__ scales) {
+__global__ __launch_bounds__(1024) void tiles_kernel(Mx4Args a, int E, int K, int ntn, float per_cu, int cap,
+                                                     int32_t* __restrict__ ws, int32_t* __restrict__ xrows,
+                                                     uint8_t* __restrict__ scales) {
   const int P = a.P;
   if (blockIdx.x > 0) {
     const int D = (K + 255) / 256, nd = (D + kPer - 1) / kPer;
@@ -107,27 +118,41 @@ __global__ __launch_bounds__(1024) void tiles_kernel(Mx4Args a, int E, int K, in
     return;
   }
   const int32_t* offsets = a.offsets;
-  __shared__ int wave_tot[16];
+  __shared__ v4u wave_tot[16];
   const int e = threadIdx.x, lane = e & 63, w = e >> 6;
   int begin = 0, n = 0;
   if (e < E) {
     begin = min(max(offsets[e], 0), P);
     n = min(max(offsets[e + 1], begin), P) - begin;
   }
-  const int nt = (n + kBM - 1) / kBM;
-  const int incl = wave_inclusive_scan(nt, lane);
-  if (lane == 63) wave_tot[w] = incl;
-  __syncthreads();
-  int at = incl - nt, total = 0;
-  for (int i = 0; i < 16; ++i) {
-    if (i < w) at += wave_tot[i];
-    total += wave_tot[i];
+  uint32_t count[4], incl[4];  // tiles of at most 64 (i + 1) rows (a wave's sum stays below 2^32)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    count[i] = (n + 64 * i + 63) / (64 * (i + 1));
+    incl[i] = (uint32_t)wave_inclusive_scan((int)count[i], lane);
   }
-  if (e == 0) ws[0] = min(total, cap);
+  if (lane == 63) wave_tot[w] = v4u{incl[0], incl[1], incl[2], incl[3]};
+  __syncthreads();
+  // offsets that decrease could name more tiles than the list holds, or than 32 bits count
+  v4u before = {0, 0, 0, 0}, all = {0, 0, 0, 0};
+  for (int v = 0; 64 * v < E; ++v) {
+    const v4u t = wave_tot[v];
+    if (v == w) before = all;
+    all = __builtin_elementwise_add_sat(all, t);
+  }
+  uint32_t nt = 0, at = 0, total = 0;
+  float best = 0.0f;
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    const float units = item_units(all[i], ntn, per_cu, i + 1);
+    if (i == 3 || units < best)
+      best = units, nt = count[i], at = __builtin_elementwise_add_sat(before[i], incl[i] - nt), total = all[i];
+  }
+  if (e == 0) ws[0] = min(total, (uint32_t)cap);
   const int h = nt > 0 ? tile_height(n, nt) : 0;
   int4* list = reinterpret_cast<int4*>(ws) + 1;
-  // offsets that decrease could name more tiles than the list holds
-  for (int i = 0; i < nt && at + i < cap; ++i) list[at + i] = make_int4(e, begin + i * h, min(h, n - i * h), 0);
+  for (int i = 0; i < (int)nt; ++i)
+    if (__builtin_elementwise_add_sat(at, (uint32_t)i) < (uint32_t)cap) list[at + i] = make_int4(e, begin + i * h, min(h, n - i * h), 0);
 }
 
 typedef __attribute__((address_space(4))) const int32_t cint;  // read by scalar loads
@@ -723,19 +748,14 @@ int workgroups() {
   return n;
 }
 
-// Row tiles of a dense product of P rows and ntn columns of items.  An item of
-// up to s sub-tiles per SIMD (64 s rows) takes about 7 + 2 s units (K 7168, N
-// 2048, 512 rows: 39 us with s = 4, 28 with 2, 23 with 1: what does not shrink
-// is the wait for its loads), and the items run in rounds of one per CU; the
-// fewest units win, larger tiles on a tie.  K 7168, N 2048, 1024 rows: 24 us
-// against 39 with tiles of 256 rows; K 4096, N 1536, 4604 rows: 25 against 29.
+// Row tiles of a dense product of P rows and ntn columns of items.
 int dense_tiles(int P, int ntn) {
-  const int n32 = (P + 31) / 32, cus = workgroups();
-  int best = 0, tiles = 1;
+  int tiles = 0;
+  float best = 0.0f;
   for (int s = 4; s > 0; --s) {
-    const int t = (n32 + 2 * s - 1) / (2 * s);
-    const long units = ((long)t * ntn + cus - 1) / cus * (7 + 2 * s);
-    if (best == 0 || units < best) best = (int)min(units, 0x7FFFFFFFl), tiles = t;
+    const int t = (P + 64 * s - 1) / (64 * s);
+    const float units = item_units(t, ntn, 1.0f / (float)workgroups(), s);
+    if (s == 4 || units < best) best = units, tiles = t;
   }
   return tiles;
 }
@@ -745,13 +765,14 @@ int dense_tiles(int P, int ntn) {
 size_t mx4_tiled_ws_bytes(long P, int E, int K) { return scales_at(P, E) + 8 * (size_t)P * ((K + 255) / 256); }
 
 hipError_t launch_mx4_tiled(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, void* ws, hipStream_t st) {
+  const int ntn = (L.NT + kBT - 1) / kBT;
   Launch g{a, L, nullptr, nullptr, a.xs, 8, L.K / 32, 0, 0};
   if (a.offsets) {
     int32_t* list = static_cast<int32_t*>(ws);
     int32_t* xrows = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + rows_at(a.P, L.E));
     uint8_t* scales = static_cast<uint8_t*>(ws) + scales_at(a.P, L.E);
     const size_t threads = (size_t)a.P * ((L.D + kPer - 1) / kPer);
-    hipLaunchKernelGGL(tiles_kernel, dim3((unsigned)(1 + (threads + 1023) / 1024)), dim3(1024), 0, st, a, L.E, L.K,
+    hipLaunchKernelGGL(tiles_kernel, dim3((unsigned)(1 + (threads + 1023) / 1024)), dim3(1024), 0, st, a, L.E, L.K, ntn, 1.0f / (float)workgroups(),
                        (int)tile_cap(a.P, L.E), list, xrows, scales);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -761,7 +782,7 @@ hipError_t launch_mx4_tiled(const Mx4Args& a, const Mx4Layout& L, bool fp32_out,
     g.scale_stage = 8 * (size_t)a.P;
     g.scale_row = 8;
   } else {
-    g.tiles = dense_tiles(a.P, (L.NT + kBT - 1) / kBT);
+    g.tiles = dense_tiles(a.P, ntn);
     g.height = tile_height(a.P, g.tiles);
   }
   const dim3 grid((unsigned)workgroups()), block(64 * kWaves);

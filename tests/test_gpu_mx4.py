@@ -264,6 +264,12 @@ def test_grouped_many_items(dev, K, gather):
     group_case(dev, sizes, K, 4096 + 32, False, gather, "bf16", PREFILL, lead=2, tail=3)
 
 
+@pytest.mark.parametrize("glu", [False, True])
+def test_grouped_tall_tiles(dev, glu):
+    """Items enough for the tallest tiles, whole and with their last rows missing."""
+    group_case(dev, [1024, 768, 256, 250], 256, 3584 if glu else 7168, glu, None, "bf16", PREFILL, lead=1, tail=2)
+
+
 def test_grouped_no_rows(dev):
     r = rng(3)
     wq, ws, _ = weights4(r, 4, 64, 256)
