@@ -2,7 +2,7 @@
 // same packed weights): LDS-tiled, bound by the FP4 matrix rate, or by HBM
 // where an expert's rows are few.
 //
-// A work item is 256 rows of one group x 8 weight tiles (256 weight rows).
+// A work item is up to 256 rows of one group x 8 weight tiles (256 weight rows).
 // Eight waves, two per SIMD, in a 4 x 2 grid, each with up to two 32-token
 // sub-tiles x four weight tiles: 8 accumulators of 32 x 32 (128 registers).
 // v_mfma_scale_f32_32x32x64_f8f6f4 rather than 16x16x128: it lasts 32 clocks
@@ -31,9 +31,9 @@
 //
 // Measured (one call): 4604 rows, K 16384, N 7168: 244 us, 4.4 PFLOP/s with the
 // matrix units 65 % busy at the 1.58 GHz that the power limit leaves.  SwiGLU
-// of 4604 tokens x 8 of 256 experts, K 7168, N 2048: 848 us, 5.6 TB/s of HBM.
-// 16384 tokens x 8 of 256 experts (Zipf), K 2048, N 7168: 1246 us, 3.1 PFLOP/s
-// and 4.0 TB/s.  The same tile by four waves of 64 x 256, one per SIMD: 277, 1058 and
+// of 4604 tokens x 8 of 256 experts, K 7168, N 2048: 849 us, 5.6 TB/s of HBM.
+// 16384 tokens x 8 of 256 experts (Zipf), K 2048, N 7168: 1268 us, 3.0 PFLOP/s
+// and 3.9 TB/s.  The same tile by four waves of 64 x 256, one per SIMD: 277, 1058 and
 // 1490 us before the later steps, against 283, 960 and 1362 with eight waves
 // and stages of 128 bytes a row; 192 rows with three row stages is 3-15 %
 // slower.
