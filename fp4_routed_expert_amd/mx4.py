@@ -19,39 +19,38 @@ from . import _lib
 _TYPES = {torch.bfloat16: _lib.MOE_TYPE_BF16, torch.float16: _lib.MOE_TYPE_FP16, torch.float32: _lib.MOE_TYPE_FP32}
 _QUANT = {None: _lib.MOE_QUANT_NONE, "mxfp8": _lib.MOE_QUANT_MXFP8, "mxfp4": _lib.MOE_QUANT_MXFP4}
 _NORM_DTYPES = (torch.bfloat16, torch.float32)
+_U8 = (torch.uint8,)
 
 
 def _need(t: torch.Tensor, name: str, dtypes, shape, dev=None):
     """Type, shape and device of a contiguous argument; its address."""
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and (t.is_cuda if dev is None else t.device == dev):
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: contiguous tensor required")
-    if not t.is_cuda or (dev is not None and t.device != dev):
-        raise ValueError(f"{name}: on {t.device}, not on {dev if dev is not None else 'a GPU'}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on {t.device}, not on {dev if dev is not None else 'a GPU'}")
 
 
-# The current stream's handle without a Stream object around it, where torch has it.
+# The current device and its stream's handle without the objects around them, where torch has these.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _call(name: str, dev: torch.device, *args):
     """One library call on dev's current stream, dev being the current device meanwhile."""
     fn = getattr(_lib.lib(), name)
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, _stream(dev.index))
+    i = dev.index
+    if i == _device():
+        status = fn(*args, _stream(i))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, _stream(dev.index))
+            status = fn(*args, _stream(i))
     if status:
         _lib.check(status, name)
-
-
-def _u8(t, name, shape, dev):
-    return _need(t, name, (torch.uint8,), shape, dev)
 
 
 def _workspace(ws, need, dev):
@@ -79,7 +78,7 @@ def quant_mxfp4(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tensor 
         q = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
     if s is None:
         s = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
-    qp, sp = _u8(q, "q", (M, K // 2), dev), _u8(s, "s", (M, K // 32), dev)
+    qp, sp = _need(q, "q", _U8, (M, K // 2), dev), _need(s, "s", _U8, (M, K // 32), dev)
     _call("moe_quant_mxfp4", dev, x.data_ptr(), _TYPES[x.dtype], M, K, x.stride(0) if M > 1 else K, qp, sp)
     return q, s
 
@@ -96,8 +95,8 @@ def dequant_mx(q: torch.Tensor, s: torch.Tensor, format: str, dtype: torch.dtype
     dev = q.device
     if out is None:
         out = torch.empty((M, K), dtype=dtype, device=dev)
-    qp = _u8(q, "q", (M, K // 2 if format == "mxfp4" else K), None)
-    sp, op = _u8(s, "s", (M, K // 32), dev), _need(out, "out", _TYPES, (M, K), dev)
+    qp = _need(q, "q", _U8, (M, K // 2 if format == "mxfp4" else K), None)
+    sp, op = _need(s, "s", _U8, (M, K // 32), dev), _need(out, "out", _TYPES, (M, K), dev)
     _call("moe_dequant_mx", dev, qp, sp, _QUANT[format], M, K, op, _TYPES[out.dtype])
     return out
 
@@ -132,9 +131,9 @@ def _prepack(wq, ws, uq, us) -> Mxfp4Weights:
     E, N, K = (wq.shape[0] if wq.dim() == 3 else 1), wq.shape[-2], wq.shape[-1] * 2
     dev = wq.device
     sshape = wq.shape[:-1] + (K // 32,)
-    ptr = [_u8(wq, "wq", wq.shape, None), _u8(ws, "ws", sshape, dev), None, None]
+    ptr = [_need(wq, "wq", _U8, wq.shape, None), _need(ws, "ws", _U8, sshape, dev), None, None]
     if uq is not None:
-        ptr[2:] = [_u8(uq, "uq", wq.shape, dev), _u8(us, "us", sshape, dev)]
+        ptr[2:] = [_need(uq, "uq", _U8, wq.shape, dev), _need(us, "us", _U8, sshape, dev)]
     nbytes = _lib.lib().moe_mxfp4_packed_bytes(E, N, K, int(uq is not None))
     if nbytes == 0:
         raise _lib.MoeError(_lib.MOE_ERR_UNSUPPORTED, "moe_mxfp4_packed_bytes")
@@ -161,7 +160,7 @@ def mxfp4_dense(w: Mxfp4Weights, xq: torch.Tensor, xs: torch.Tensor, dtype: torc
     T, dev = xq.shape[0], xq.device
     if y is None:
         y = torch.empty((T, w.N), dtype=dtype, device=dev)
-    xp, sp = _u8(xq, "xq", (T, w.K // 2), w.buffer.device), _u8(xs, "xs", (T, w.K // 32), dev)
+    xp, sp = _need(xq, "xq", _U8, (T, w.K // 2), w.buffer.device), _need(xs, "xs", _U8, (T, w.K // 32), dev)
     yp = _need(y, "y", _NORM_DTYPES, (T, w.N), dev)
     _call("moe_mxfp4_dense_forward", dev, ctypes.byref(w.desc), xp, sp, T, yp, _TYPES[y.dtype], flags)
     return y
@@ -181,7 +180,7 @@ def mxfp4_grouped(w: Mxfp4Weights, xq: torch.Tensor, xs: torch.Tensor, offsets: 
     P = X if rows is None else rows.shape[0]
     if y is None:
         y = torch.empty((P, w.N), dtype=dtype, device=dev)
-    xp, sp = _u8(xq, "xq", (X, w.K // 2), w.buffer.device), _u8(xs, "xs", (X, w.K // 32), dev)
+    xp, sp = _need(xq, "xq", _U8, (X, w.K // 2), w.buffer.device), _need(xs, "xs", _U8, (X, w.K // 32), dev)
     op = _need(offsets, "offsets", (torch.int32,), (w.E + 1,), dev)
     rp = None if rows is None else _need(rows, "rows", (torch.int32,), (P,), dev)
     yp = _need(y, "y", _NORM_DTYPES, (P, w.N), dev)
@@ -207,7 +206,7 @@ def _norm_outputs(T, H, dev, quant, z, q, s, want_z):
             q = torch.empty((T, width), dtype=torch.uint8, device=dev)
         if s is None:
             s = torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
-        ptr[1:] = [_u8(q, "q", (T, width), dev), _u8(s, "s", (T, H // 32), dev)]
+        ptr[1:] = [_need(q, "q", _U8, (T, width), dev), _need(s, "s", _U8, (T, H // 32), dev)]
     return z, q, s, ptr
 
 
