@@ -29,11 +29,11 @@
 // so that an item's first stages arrive under the last steps and the stores of
 // the one before.
 //
-// Measured (one call): 4604 rows, K 16384, N 7168: 244 us, 4.4 PFLOP/s with the
+// Measured (one call): 4604 rows, K 16384, N 7168: 239 us, 4.5 PFLOP/s with the
 // matrix units 65 % busy at the 1.58 GHz that the power limit leaves.  SwiGLU
-// of 4604 tokens x 8 of 256 experts, K 7168, N 2048: 849 us, 5.6 TB/s of HBM.
-// 16384 tokens x 8 of 256 experts (Zipf), K 2048, N 7168: 1268 us, 3.0 PFLOP/s
-// and 3.9 TB/s.  The same tile by four waves of 64 x 256, one per SIMD: 277, 1058 and
+// of 4604 tokens x 8 of 256 experts, K 7168, N 2048: 816 us, 5.8 TB/s of HBM.
+// 16384 tokens x 8 of 256 experts (Zipf), K 2048, N 7168: 1215 us, 3.2 PFLOP/s
+// and 4.0 TB/s.  The same tile by four waves of 64 x 256, one per SIMD: 277, 1058 and
 // 1490 us before the later steps, against 283, 960 and 1362 with eight waves
 // and stages of 128 bytes a row; 192 rows with three row stages is 3-15 %
 // slower.
@@ -574,7 +574,9 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 // the group's f tiles are f neighbouring columns, so a half-wave's store covers
 // a whole run of 128 (64 with SwiGLU) outputs.  base (uniform): row 0 of the
 // sub-tile, the group's first column; off: the lane's bytes from there (its
-// column, and 4 g rows down); left: rows of the sub-tile that exist.
+// column, and 4 g rows down); left: rows of the sub-tile that exist.  The stores
+// are non-temporal: the outputs would push rows and weights out of L2 (16384
+// tokens Zipf 1279 -> 1247 us, SwiGLU 867 -> 853, dense 282 -> 277, back to back).
 template <bool kGlu, bool kF32, bool kMask>
 __device__ __forceinline__ void store_sub(const v16f (&acc)[4], gbyte* base, size_t row_bytes, uint32_t off, int left,
                                           int f) {
@@ -590,9 +592,9 @@ __device__ __forceinline__ void store_sub(const v16f (&acc)[4], gbyte* base, siz
         global<float>* q = reinterpret_cast<global<float>*>(y);
         if (!kMask || f == kO) {
           if constexpr (kGlu)
-            *reinterpret_cast<global<v2f>*>(q) = v2f{o[0], o[1]};
+            __builtin_nontemporal_store(v2f{o[0], o[1]}, reinterpret_cast<global<v2f>*>(q));
           else
-            *reinterpret_cast<global<v4f>*>(q) = v4f{o[0], o[1], o[2], o[3]};
+            __builtin_nontemporal_store(v4f{o[0], o[1], o[2], o[3]}, reinterpret_cast<global<v4f>*>(q));
         } else {
 #pragma unroll
           for (int t = 0; t < kO - 1; ++t)
@@ -602,9 +604,10 @@ __device__ __forceinline__ void store_sub(const v16f (&acc)[4], gbyte* base, siz
         global<uint16_t>* q = reinterpret_cast<global<uint16_t>*>(y);
         if (!kMask || f == kO) {
           if constexpr (kGlu)
-            *reinterpret_cast<global<uint32_t>*>(q) = f32x2_to_bf16(o[0], o[1]);
+            __builtin_nontemporal_store((uint32_t)f32x2_to_bf16(o[0], o[1]), reinterpret_cast<global<uint32_t>*>(q));
           else
-            *reinterpret_cast<global<v2u>*>(q) = v2u{f32x2_to_bf16(o[0], o[1]), f32x2_to_bf16(o[2], o[3])};
+            __builtin_nontemporal_store(v2u{f32x2_to_bf16(o[0], o[1]), f32x2_to_bf16(o[2], o[3])},
+                                        reinterpret_cast<global<v2u>*>(q));
         } else {
 #pragma unroll
           for (int t = 0; t < kO - 1; ++t)
