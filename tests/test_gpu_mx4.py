@@ -270,6 +270,23 @@ def test_grouped_tall_tiles(dev, glu):
     group_case(dev, [1024, 768, 256, 250], 256, 3584 if glu else 7168, glu, None, "bf16", PREFILL, lead=1, tail=2)
 
 
+@pytest.mark.parametrize("flags", [DECODE, PREFILL])
+def test_scales_at_any_dword(dev, flags):
+    """Activation scales need 4-byte alignment only: shifted copies give the same bits."""
+    r = rng(43)
+    P, K = 70, 1024
+    xq, xs, _ = rows4(r, P, K)
+    wq, ws, _ = weights4(r, 2, 64, K)
+    pw, one = moe.mxfp4_prepack(dev_t(wq, dev), dev_t(ws, dev)), moe.mxfp4_prepack(dev_t(wq[0], dev), dev_t(ws[0], dev))
+    q, s, off = dev_t(xq, dev), dev_t(xs, dev), dev_t(np.array([0, 33, P], np.int32), dev)
+    want, dense = moe.mxfp4_grouped(pw, q, s, off, flags=flags), moe.mxfp4_dense(one, q, s, flags=flags)
+    for shift in (4, 8, 12):
+        t = torch.empty(s.numel() + shift, dtype=torch.uint8, device=dev)[shift:].view(s.shape)
+        t.copy_(s)
+        assert torch.equal(moe.mxfp4_grouped(pw, q, t, off, flags=flags), want)
+        assert torch.equal(moe.mxfp4_dense(one, q, t, flags=flags), dense)
+
+
 def test_grouped_no_rows(dev):
     r = rng(3)
     wq, ws, _ = weights4(r, 4, 64, 256)
