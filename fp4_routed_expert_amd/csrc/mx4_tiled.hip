@@ -33,7 +33,7 @@
 // matrix units 65 % busy at the 1.58 GHz that the power limit leaves.  SwiGLU
 // of 4604 tokens x 8 of 256 experts, K 7168, N 2048: 816 us, 5.8 TB/s of HBM.
 // 16384 tokens x 8 of 256 experts (Zipf), K 2048, N 7168: 1215 us, 3.2 PFLOP/s
-// and 4.0 TB/s.  The same tile by four waves of 64 x 256, one per SIMD: 277, 1058 and
+// and 3.5 TB/s.  The same tile by four waves of 64 x 256, one per SIMD: 277, 1058 and
 // 1490 us before the later steps, against 283, 960 and 1362 with eight waves
 // and stages of 128 bytes a row; 192 rows with three row stages is 3-15 %
 // slower.
