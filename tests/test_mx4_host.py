@@ -122,8 +122,8 @@ def test_grouped_refusals():
     size = L.moe_mxfp4_grouped_workspace_size
     assert size(-1, 4, 64, 256, 0) == 0 and size(4, 0, 64, 256, 0) == 0 and size(4, 4, 63, 256, 0) == 0
     d, ws = _desc(E=4), size(1000, 4, 64, 256, 0)
-    # the list of row tiles: one for each 256 rows and each group, never fewer than the groups can have
-    assert ws >= 16 + 16 * (1000 // 256 + 4)
+    # the list of row tiles: one for each 64 rows and each group, never fewer than the groups can have
+    assert ws >= 16 + 16 * (1000 // 64 + 4)
     ok = (1000, A, A, 2, 1000, A, BF, A, ws, 0)
 
     def call(desc=d, X=1000, off=A, rows=A, div=2, P=1000, y=A, yt=BF, w=A, nb=ws, fl=0, xq=A, xs=A):
@@ -143,6 +143,7 @@ def test_grouped_refusals():
     assert call(w=NUL) == WSE
     assert call(w=ctypes.c_void_p((1 << 20) + 16)) == INV
     assert call(X=1 << 25) == UNS
+    assert call(P=(1 << 31) - 1) == UNS and size((1 << 31) - 1, 4, 64, 256, 0) == 0   # tile ends past 32 bits
     assert call(P=0, y=NUL, off=NUL, w=NUL, nb=0) == 0
 
 
