@@ -104,6 +104,12 @@ __device__ __forceinline__ void mx4_block8(const float (&v)[8], uint32_t amax, u
   scale = ef == 255 ? 255 : c;
 }
 
+// The pass behind the one at row m0 in a workgroup's walk over rows of a group,
+// end where there is none (m0 + stride may not fit in 32 bits then).
+__host__ __device__ __forceinline__ int next_pass(int m0, int stride, int end) {
+  return end - m0 > stride ? m0 + stride : end;
+}
+
 // ---------------------------------------------------------------- launchers
 hipError_t launch_mx4_quant(const void* x, ElemType type, long M, int K, long ldx, uint8_t* q, uint8_t* s,
                             hipStream_t st);

@@ -16,7 +16,8 @@ bool known_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_FP16 || 
 bool norm_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_FP32; }
 
 constexpr int kMaxMx4E = 1024;
-constexpr int kMaxMx4P = INT32_MAX - 256;  // a tile past the last row still counts in 32 bits
+// A tile past the last row still counts in 32 bits; the streaming product's passes step by next_pass.
+constexpr int kMaxMx4P = INT32_MAX - 256;
 constexpr int kMaxNormH = 16384;
 
 // A grid of one workgroup of 256 threads per 1024 groups of eight elements has

@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(Mx4Args a, Mx4Layout L)
     wt[t] = a.packed + L.tile_off(e, min(nt0 + t, L.NT - 1)) + 16 * lane;
   const uint8_t* st = a.packed + L.scale_off(e, nt0 >> 2) + 16 * lane + 2 * (nt0 & 3);
   const int nsteps = J > wave ? (J - wave + NW - 1) / NW : 0;
-  for (int m0 = begin; m0 < end; m0 += stride) {
+  for (int m0 = begin; m0 < end; m0 = next_pass(m0, stride, end)) {
     const int rows = min(kRows, end - m0);
     int xr = m0 + min(n, rows - 1);
     if (a.rows) xr = (int)((unsigned)a.rows[xr] / (unsigned)a.div);

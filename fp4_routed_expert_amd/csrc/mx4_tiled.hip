@@ -785,7 +785,7 @@ hipError_t launch_mx4_tiled(const Mx4Args& a, const Mx4Layout& L, bool fp32_out,
     int32_t* list = static_cast<int32_t*>(ws);
     int32_t* xrows = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + rows_at(a.P, L.E));
     uint8_t* scales = static_cast<uint8_t*>(ws) + scales_at(a.P, L.E);
-    const dim3 movers(1 + (unsigned)(a.P + 1023) / 1024, (unsigned)(L.D + kPer - 1) / kPer);
+    const dim3 movers(1 + ((unsigned)a.P + 1023u) / 1024, (unsigned)(L.D + kPer - 1) / kPer);
     const bool wide = L.K % 512 == 0 && (uintptr_t)a.xs % 16 == 0;
     hipLaunchKernelGGL(tiles_kernel, movers, dim3(1024), 0, st, a, L.E, L.K, ntn, 1.0f / (float)workgroups(),
                        (int)tile_cap(a.P, L.E), wide, list, xrows, scales);
