@@ -80,6 +80,12 @@ int select_path(int64_t P, int E, uint32_t flags) {
   return P <= kDecodeRowsPerExpert * (int64_t)E ? 0 : 1;
 }
 
+// The prefill kernels address activation rows with 32-bit offsets.  Calls that
+// enqueue other stages in front of expert_up check this before the first one.
+bool rows_past_32_bits(int path, int32_t T, int32_t H) {
+  return path == 1 && (int64_t)T * H >= ((int64_t)1 << 32);
+}
+
 size_t stage_ws_bytes(int32_t T, int32_t k, int32_t E, int32_t H, int32_t I) {
   return align256(prefill_stage_bytes((long)T * k, E, H, I));
 }
@@ -302,8 +308,7 @@ static moe_status_t expert_up(const moe_fp4_weights_t* w, const uint8_t* xq, con
   if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
   const PackedLayout L(w->E, w->H, w->I);
   const uint8_t* pk = static_cast<const uint8_t*>(w->packed);
-  // the prefill kernel addresses activation rows with 32-bit offsets
-  if (path == 1 && (int64_t)T * w->H >= ((int64_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+  if (rows_past_32_bits(path, T, w->H)) return MOE_ERR_UNSUPPORTED;
   if (path == 1)
     return hip_status(launch_up_prefill(pk, L, xq, xs, expert_offsets, sorted_pair, T, k, hq, hs,
                                         hs_by_step, workspace, stream));
@@ -428,7 +433,8 @@ moe_status_t moe_fp4_layer_forward(const moe_fp4_weights_t* w, const uint16_t* x
   if (st != MOE_OK) return st;
   st = check_tek(T, w->E, k);
   if (st != MOE_OK) return st;
-  if (select_path((int64_t)T * k, w->E, flags) < 0) return MOE_ERR_INVALID_ARGUMENT;
+  const int path = select_path((int64_t)T * k, w->E, flags);
+  if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
   if (T == 0) return MOE_OK;
   if (!x_bf16 || !logits || !y) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(x_bf16, 16) || !aligned(logits, 4) || !aligned(y, 16))
@@ -437,6 +443,7 @@ moe_status_t moe_fp4_layer_forward(const moe_fp4_weights_t* w, const uint16_t* x
   const LayerCarve c = layer_carve(T, k, E, H, I);
   if (!workspace || workspace_bytes < c.total) return MOE_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows_past_32_bits(path, T, H)) return MOE_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   st = run_front(logits, 1, x_bf16, T, H, E, k, 0, ws, c, stream);
   if (st != MOE_OK) return st;
@@ -553,13 +560,15 @@ moe_status_t moe_fp4_shared_expert(const moe_fp4_weights_t* w, const uint8_t* xq
   if (w->E != 1) return MOE_ERR_INVALID_ARGUMENT;
   st = check_tek(T, 1, 1);
   if (st != MOE_OK) return st;
-  if (select_path(T, 1, flags) < 0) return MOE_ERR_INVALID_ARGUMENT;
+  const int path = select_path(T, 1, flags);
+  if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
   if (T == 0) return MOE_OK;
   if (!xq || !xs || !O_shared) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(O_shared, 16)) return MOE_ERR_INVALID_ARGUMENT;
   const SharedCarve c = shared_carve(T, w->H, w->I);
   if (!workspace || workspace_bytes < c.total) return MOE_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows_past_32_bits(path, T, w->H)) return MOE_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int32_t* sorted = reinterpret_cast<int32_t*>(ws + c.sorted);
   int32_t* offsets = reinterpret_cast<int32_t*>(ws + c.offsets);
@@ -610,7 +619,8 @@ moe_status_t moe_fp4_layer_forward_full(const moe_fp4_weights_t* w, int32_t n_sh
   st = check_full(T, k, w->E, w->H, n_shared);
   if (st != MOE_OK) return st;
   const int32_t E = w->E, H = w->H, I = w->I, ns = n_shared, Er = E - ns, kk = k + ns;
-  if (select_path((int64_t)T * kk, E, flags) < 0) return MOE_ERR_INVALID_ARGUMENT;
+  const int path = select_path((int64_t)T * kk, E, flags);
+  if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
   if (T == 0) return MOE_OK;
   if (!router_w || !x_bf16 || !y) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(router_w, 16) || !aligned(x_bf16, 16) || !aligned(y, 16))
@@ -618,6 +628,7 @@ moe_status_t moe_fp4_layer_forward_full(const moe_fp4_weights_t* w, int32_t n_sh
   const FullCarve c = full_carve(T, k, E, H, I, ns);
   if (!workspace || workspace_bytes < c.total) return MOE_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows_past_32_bits(path, T, H)) return MOE_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* rout = reinterpret_cast<float*>(ws + c.rout);
   const int S = router_slices(T, H, Er);
@@ -733,7 +744,8 @@ moe_status_t moe_fp4_block_forward(const moe_fp4_weights_t* w, int32_t n_shared,
   st = check_full(T, k, w->E, w->H, n_shared);
   if (st != MOE_OK) return st;
   const int32_t E = w->E, H = w->H, I = w->I, ns = n_shared, Er = E - ns, kk = k + ns;
-  if (select_path((int64_t)T * kk, E, flags) < 0 || !n) return MOE_ERR_INVALID_ARGUMENT;
+  const int path = select_path((int64_t)T * kk, E, flags);
+  if (path < 0 || !n) return MOE_ERR_INVALID_ARGUMENT;
   if (T == 0) return MOE_OK;
   if (!router_w || !aligned(router_w, 16)) return MOE_ERR_INVALID_ARGUMENT;
   const BlockCarve c = block_carve(T, k, E, H, I, ns);
@@ -752,6 +764,7 @@ moe_status_t moe_fp4_block_forward(const moe_fp4_weights_t* w, int32_t n_shared,
     st = check_norm_before(x, x_type, n->w_pre, n->w_type, T, H, n->eps, z, lw + lc.xq, lw + lc.xs,
                            MOE_QUANT_MXFP8);
   if (st != MOE_OK) return st;
+  if (rows_past_32_bits(path, T, H)) return MOE_ERR_UNSUPPORTED;
   // few tokens: the layer's fused front quantises z itself; otherwise the norm
   // writes the experts' rows beside z (the same bytes, z is not read again)
   const bool small = T <= kFrontMaxT;
