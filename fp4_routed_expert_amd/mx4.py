@@ -151,6 +151,8 @@ def mxfp4_prepack(wq: torch.Tensor, ws: torch.Tensor) -> Mxfp4Weights:
 
 def mxfp4_prepack_glu(wq, ws, uq, us) -> Mxfp4Weights:
     """Gate (wq, ws) and up (uq, us) weights of one shape: the products return silu(gate) * up."""
+    if uq is None or us is None:
+        raise ValueError("uq, us: the up projection's weights required (mxfp4_prepack for plain ones)")
     return _prepack(wq, ws, uq, us)
 
 
