@@ -60,9 +60,9 @@ constexpr int kState = kInfo + kWaves * 128; // and where its cursor goes next
 constexpr int kLds = kState + kWaves * 64;
 static_assert(kStage % 1024 == 0 && kLds <= 160 * 1024, "LDS");
 
-// A group's tiles of at most 256 rows are of equal heights.
+// Rows of an item.  A group's tiles of at most 256 rows are of equal heights.
 struct Tile {
-  int e, row0, n;
+  int row0, n;
 };
 
 // Rows of each tile of a group of n rows, in whole sub-tiles of 32.
@@ -473,7 +473,6 @@ __device__ __forceinline__ void read_frag(Frag& f, uint32_t xa, uint32_t wa, int
     f.x[q - 4] = lds_v4(xa + 4096 * (q - 4));
 }
 
-template <int S>
 __device__ __forceinline__ void read_scales(Scales& s, uint32_t stage, const Addr& ad, v4u& raw) {
   raw = lds_v4(stage + ad.sa);
   s.w = lds_v4(stage + ad.sw);
@@ -487,15 +486,11 @@ __device__ __forceinline__ void shift_scales(Scales& s, const Addr& ad, const v4
   }
 }
 
-// MFMA m (an item's first ones, kInit, add to zero) of K-half kHalf of step H: sub-tile m / 4, tile m % 4 (whose scale is
+// MFMA m of K-half kHalf of step H: sub-tile m / 4, tile m % 4 (whose scale is
 // byte 2 (m % 2) + kHalf of its pair's dword).
-template <int H, int kHalf, bool kInit>
+template <int H, int kHalf>
 __device__ __forceinline__ void multiply(v16f (&acc)[2][4], const Frag& f, const Scales& s, int m) {
   const int i = m >> 2, t = m & 3;
-  if constexpr (kInit) {
-#pragma unroll
-    for (int v = 0; v < 16; ++v) acc[i][t][v] = 0.0f;
-  }
   if (t & 1)
     mfma<kHalf, 2 + kHalf>(acc[i][t], f.x[i], f.w[t], s.x[i][H], s.w[2 * H + (t >> 1)]);
   else
@@ -508,7 +503,7 @@ __device__ __forceinline__ void multiply(v16f (&acc)[2][4], const Frag& f, const
 // this one is; in step 0 its first step's weights (whose place is free behind
 // the barrier), in step 1 the row pieces and, in the next stage's step 0, the
 // rest, spread over the MFMAs.
-template <int S, int H, bool kInit>
+template <int S, int H>
 __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, uint32_t cur, uint32_t nxt,
                                      v16f (&acc)[2][4], Frag& f0, Frag& f1, Scales& s) {
   constexpr int M = 4 * S;  // MFMAs of a half
@@ -518,7 +513,7 @@ __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, ui
     const uint32_t xa = cur + ad.a[2 * H + 1], wa = cur + ad.w + (uint32_t)(H * kW + 1024);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      multiply<H, 0, kInit>(acc, f0, s, m);
+      multiply<H, 0>(acc, f0, s, m);
 #pragma unroll
       for (int q = 0; q < R; ++q)
         if (q * M / R == m) read_frag(f1, xa, wa, q);
@@ -552,10 +547,10 @@ __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, ui
     Scales ns;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      multiply<H, 1, false>(acc, f1, s, m);
+      multiply<H, 1>(acc, f1, s, m);
       if (m == 0) {
         publish();
-        if constexpr (H == 1) read_scales<S>(ns, nxt, ad, raw);
+        if constexpr (H == 1) read_scales(ns, nxt, ad, raw);
       }
 #pragma unroll
       for (int q = 0; q < R; ++q)
@@ -645,7 +640,7 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][q][v] = 0.0f;
     v4u raw;
-    read_scales<S>(s, cur, ad, raw);
+    read_scales(s, cur, ad, raw);
 #pragma unroll
     for (int q = 0; q < S + 4; ++q) read_frag(f0, cur + ad.a[0], cur + ad.w, q);
     shift_scales<S>(s, ad, raw);
@@ -653,8 +648,8 @@ __device__ __forceinline__ void run_item(const Ctx& c, Cursor& k, const Addr& ad
   for (int d = 0; d < c.D; ++d) {
     cur = wave_u32(c.lds + (uint32_t)(stage * kStage));
     nxt = wave_u32(c.lds + (uint32_t)((stage ^ 1) * kStage));
-    step<S, 0, false>(c, k, ad, cur, nxt, acc, f0, f1, s);
-    step<S, 1, false>(c, k, ad, cur, nxt, acc, f0, f1, s);
+    step<S, 0>(c, k, ad, cur, nxt, acc, f0, f1, s);
+    step<S, 1>(c, k, ad, cur, nxt, acc, f0, f1, s);
     stage ^= 1;
   }
   if constexpr (S > 0) {
@@ -731,7 +726,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
   for (int i = 0; i < mine; ++i) {
     // as the cursor noted it
     const v4u info = lds_v4(c.lds + kInfo + 128 * wave + 16 * (i & 7));
-    const Tile t{0, (int)wave_u32(info.x), (int)wave_u32(info.y)};
+    const Tile t{(int)wave_u32(info.x), (int)wave_u32(info.y)};
     const int tn = (int)wave_u32(info.z);
     const int sub0 = first_sub(t.n, wm), live = sub_tiles(t.n, wm);
     const uint32_t row = (uint32_t)(32 * sub0 + r);
