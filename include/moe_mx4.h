@@ -89,7 +89,10 @@ moe_status_t moe_mxfp4_prepack(const uint8_t* wq, const uint8_t* ws, const uint8
 /*
  * Dense product: y[t, n] = sum_k x[t, k] W[n, k] (or its SwiGLU form), both
  * operands MXFP4, accumulated in fp32 in the matrix cores and rounded once to
- * y_type (bf16, or fp32 as it is).
+ * y_type (bf16, or fp32 as it is).  SiLU takes the hardware's exponential and
+ * reciprocal: with a gate sum g, fp32 outputs are within (|g| + 8) 2^-22 of
+ * their size of silu(g) * up; below g = -87, where silu(g) < 2^-118, they may
+ * be 0.
  *   xq [T, K/2] (16-byte aligned), xs [T, K/32] (4-byte aligned)
  *   y [T, N] (16-byte aligned); T * K <= 2^33 - 8192
  *   flags: MOE_FLAG_FORCE_DECODE streams the weights for every 32 tokens,
