@@ -56,6 +56,12 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K / 2 > ((int64_
 // last pass counted half): 16 experts, K 2048, N 512, 2000 rows (1120) 12 and
 // 21; 4 experts, K 2048, N 4096, 256 rows (1280) 11 and 15; 8 experts, K 16384,
 // N 2048, 400 rows (1024) 70 and 59, K 4096, N 4096, 512 rows (2560) 47 and 30.
+// The averages do not see skew, which only the device knows: streaming walks a
+// group's rows 32 at a time, by one workgroup per tile pair once the groups' tiles
+// fill the CUs.  64 experts, K 4096, N 1536, 1024 rows, even / Zipf (largest group
+// 305) / all in one group: streaming 49 / 111 / 183, tiled 43 / 42 / 20; SwiGLU 83 /
+// 137 / 259 and 84 / 82 / 22.  A caller that knows its routing to be skewed forces
+// the tiled product.
 constexpr int64_t kStreamRows = 16, kStreamPasses = 1024, kStreamGroupedPasses = 1280;
 int choose_path(int64_t P, const Mx4Layout& L, bool grouped, uint32_t flags) {
   const bool fd = flags & MOE_FLAG_FORCE_DECODE, fp = flags & MOE_FLAG_FORCE_PREFILL;

@@ -12,8 +12,9 @@
 // block and join their maxima with two lane swaps, so that loads and stores of
 // a wave are contiguous without a trip through LDS.  Four groups per thread keep
 // 64 bytes in flight each.  Measured: 98304 x 4096 bf16 in 158 us (6.5 TB/s of
-// reads and writes), read back in 168 us (6.1 TB/s); 8 x 4096 in 2.5 us, a
-// launch.
+// reads and writes), read back in 166 us (6.2 TB/s); 8 x 4096 in 2.4 us, a
+// launch.  Rows that are further apart cost a division per group: 162 us with 4104
+// elements from row to row, 164 with 8192.
 #include "mx4.h"
 
 namespace moe {

@@ -13,7 +13,8 @@
 // tokens, but a 2 KiB tile step costs 64 clocks of one SIMD's matrix unit
 // while its share of HBM takes three times that.  Measured: K 2048, N 7168, 256
 // experts, 512 rows: 265 us, 6.5 TB/s; SwiGLU, K 4096, N 1536, 64 experts, 48
-// rows: 43 us, 5.3 TB/s; dense K 16384, N 7168, 8 rows: 15.3 us, 4.1 TB/s.
+// rows: 42 us, 5.4 TB/s; dense K 16384, N 7168, 8 rows: 15.2 us, 4.1 TB/s (14.6 and
+// 15.1 us a call back to back on one weight and on eight in turn, 0.5 GB).
 #include "mx4.h"
 
 namespace moe {
@@ -217,6 +218,8 @@ hipError_t launch_mx4_pack(const uint8_t* wq, const uint8_t* ws, const uint8_t* 
 //   2048, 256 rows (256 pairs): 14.7 with eight, 16.5 with four; 256 experts, K
 //   2048, N 7168, 512 rows: 307 and 262; 16 experts, K 16384, N 2048, 128 rows:
 //   50.6 and 55.2.
+// The counts are against the 256 CUs that these were measured on; a device with
+// fewer gets the same results.
 hipError_t launch_mx4_stream(const Mx4Args& a, const Mx4Layout& L, bool fp32_out, hipStream_t st) {
   constexpr long kCUs = 256;
   const long passes = (a.P + kRows - 1) / kRows;

@@ -177,7 +177,8 @@ def mxfp4_grouped(w: Mxfp4Weights, xq: torch.Tensor, xs: torch.Tensor, offsets: 
                   flags: int = 0, y: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """y [P, N]: row s of expert e (offsets[e] <= s < offsets[e+1]) is W[e] x[r], r = rows[s] // row_div,
     or s without ``rows``.  With sort_permute's sorted_pair and row_div = k, r is the pair's token.
-    Rows outside [offsets[0], offsets[E]) are left as they were."""
+    Rows outside [offsets[0], offsets[E]) are left as they were.  flags: MOE_FLAG_FORCE_PREFILL is faster
+    where a few experts hold most of few rows."""
     X, dev = xq.shape[0], xq.device
     P = X if rows is None else rows.shape[0]
     if y is None:

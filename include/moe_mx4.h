@@ -117,7 +117,9 @@ moe_status_t moe_mxfp4_dense_forward(const moe_mxfp4_weights_t* w /*(host), E ==
  *   workspace >= moe_mxfp4_grouped_workspace_size(P, E, N, K, glu) bytes,
  *     256-byte aligned; contents ignored on entry.  Calls (or captured graphs)
  *     that may overlap need one each.
- *   flags as above; X * K <= 2^33 - 8192, P < 2^31 - 256
+ *   flags as above; by default P, E and N decide, not the groups' sizes (which
+ *   are on the device): where a few groups hold most of few rows,
+ *   MOE_FLAG_FORCE_PREFILL is faster.  X * K <= 2^33 - 8192, P < 2^31 - 256
  */
 size_t moe_mxfp4_grouped_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K, int32_t glu);
 moe_status_t moe_mxfp4_grouped_forward(const moe_mxfp4_weights_t* w /*(host)*/, const uint8_t* xq, const uint8_t* xs,
