@@ -37,10 +37,7 @@
 // 1490 us before the later steps, against 283, 960 and 1362 with eight waves
 // and stages of 128 bytes a row; 192 rows with three row stages is 3-15 %
 // slower.
-#include <atomic>
-
-#include "lds_dma.h"
-#include "mx4.h"
+#include "tiled.h"
 
 namespace moe {
 namespace {
@@ -166,8 +163,6 @@ __global__ __launch_bounds__(1024) void tiles_kernel(Mx4Args a, int E, int K, in
     if (__builtin_elementwise_add_sat(at, (uint32_t)i) < (uint32_t)cap) list[at + i] = make_int4(e, begin + i * h, min(h, n - i * h), 0);
 }
 
-typedef __attribute__((address_space(4))) const int32_t cint;  // read by scalar loads
-
 // What a launch is given.  Only a few of these values are needed at every
 // stage; the others are read again from the kernel's arguments (by scalar
 // loads) where an item begins or ends, since scalar registers that are kept
@@ -184,30 +179,6 @@ struct Launch {
 };
 typedef __attribute__((address_space(4))) const Launch claunch;
 
-// Where a wave's walk over the items stands (in LDS between items).  The items
-// go by panels of a quarter of the columns, row tiles running inside a panel,
-// so that the items that an XCD holds at one time share rows and weights in
-// its L2.  Steps inside a panel need no division.
-struct Walk {
-  int p, hi, stride;  // item, end of this XCD's share, items from one to the next
-  int ntt, ntn;       // row tiles, weight-tile columns of eight
-  int tt, off;        // row tile, column inside the panel
-  int base, w;        // the panel's first column and its width
-  int st, so;         // stride / w, stride % w
-  int e, row0, n;     // the item's tile of rows
-  int count, more;    // items before it; whether there is one
-};
-static_assert(sizeof(Walk) == 64, "four 128-bit words");
-
-__device__ __forceinline__ void locate(Walk& k) {
-  const int sn = (k.ntn + 3) / 4, sc = k.p / (k.ntt * sn), q = k.p - sc * (k.ntt * sn);
-  k.base = sc * sn;
-  k.w = max(min(sn, k.ntn - k.base), 1);
-  k.tt = q / k.w;
-  k.off = q - k.tt * k.w;
-  k.st = k.stride / k.w;
-  k.so = k.stride - k.st * k.w;
-}
 __device__ __forceinline__ void look_up(const claunch* g, Walk& k) {
   if (g->a.offsets) {
     const cint* p = reinterpret_cast<const cint*>(reinterpret_cast<uintptr_t>(g->ws)) + 4 + 4 * k.tt;
@@ -233,17 +204,6 @@ __device__ __forceinline__ void next_item(const claunch* g, Walk& k) {
   }
   if (k.tt >= k.ntt) locate(k);
   look_up(g, k);
-}
-
-__device__ __forceinline__ uint32_t opaque(uint32_t x) {
-  asm volatile("" : "+v"(x));
-  return x;
-}
-__device__ __forceinline__ v4u lds_v4(uint32_t addr) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) v4u*>((uintptr_t)addr);
-}
-__device__ __forceinline__ int lds_i32(uint32_t addr) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) int*>((uintptr_t)addr);
 }
 
 // One MFMA, its accumulator pinned to AGPRs at this point of the program and
@@ -289,35 +249,6 @@ struct Ctx {
   }
 };
 
-// LDS-DMA: lane l's 16 (4) bytes at base + off go to LDS address lds + 16 l
-// (4 l); an instruction offset counts on both sides.  The LDS address goes to
-// M0, which nothing else here uses (LDS instructions need none).  The base is
-// copied by the scalar unit first: a scalar register that a vector instruction
-// has written (v_readfirstlane) must not be read by a load within five wait
-// states, and the compiler does not look into the asm; the copy is also the
-// wait state that M0 needs.
-template <int kOff = 0>
-__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  const uint8_t* t;
-  asm volatile(
-      "s_mov_b32 m0, %3\n\t"
-      "s_mov_b64 %0, %2\n\t"
-      "global_load_lds_dwordx4 %1, %0 offset:%4"
-      : "=&s"(t)
-      : "v"(off), "s"(wave_ptr(base)), "s"(wave_u32(lds)), "n"(kOff)
-      : "memory");
-}
-__device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
-  const uint8_t* t;
-  asm volatile(
-      "s_mov_b32 m0, %3\n\t"
-      "s_mov_b64 %0, %2\n\t"
-      "global_load_lds_dword %1, %0"
-      : "=&s"(t)
-      : "v"(off), "s"(wave_ptr(base)), "s"(wave_u32(lds))
-      : "memory");
-}
-
 // Sub-tiles of 32 rows that wave row wm (of four) takes of a tile of n rows:
 // how many, and the first one.  Wave rows 0 and 2 share SIMDs, as do 1 and 3.
 __device__ __forceinline__ int sub_tiles(int n, int wm) { return ((n + 31) / 32 + 3 - wm) / 4; }
@@ -334,24 +265,9 @@ __device__ __forceinline__ int scale_row(int n, int wave, int lane) {
   return 32 * (first_sub(n, wave >> 1) + ((at >> 1) & 1)) + (at >> 2);
 }
 
-typedef __attribute__((address_space(3))) v4u lds_words;
-__device__ __forceinline__ Walk load_walk(const Ctx& c) {
-  const lds_words* p = reinterpret_cast<const lds_words*>((uintptr_t)(c.lds + kState + 64u * (uint32_t)c.wave));
-  v4u w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = p[i];
-  Walk k;
-  int* f = reinterpret_cast<int*>(&k);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] = (int)wave_u32(w[i >> 2][i & 3]);
-  return k;
-}
+__device__ __forceinline__ Walk load_walk(const Ctx& c) { return read_walk(c.lds + kState + 64u * (uint32_t)c.wave); }
 __device__ __forceinline__ void store_walk(const Ctx& c, const Walk& k) {
-  lds_words* p = reinterpret_cast<lds_words*>((uintptr_t)(c.lds + kState + 64u * (uint32_t)c.wave));
-  const int* f = reinterpret_cast<const int*>(&k);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    p[i] = v4u{(uint32_t)f[4 * i], (uint32_t)f[4 * i + 1], (uint32_t)f[4 * i + 2], (uint32_t)f[4 * i + 3]};
+  write_walk(c.lds + kState + 64u * (uint32_t)c.wave, k);
 }
 
 // Row index DMA of the walk's item into the index buffer: each wave loads, and
@@ -570,12 +486,6 @@ __device__ __forceinline__ void step(const Ctx& c, Cursor& k, const Addr& ad, ui
   }
 }
 
-// Global (not flat) pointers: flat stores would count as LDS traffic too.
-template <class T>
-using global = __attribute__((address_space(1))) T;
-typedef global<uint8_t> gbyte;
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-
 // Stores of one sub-tile: element v of a lane is row 8 (v / 4) + 4 g + v % 4;
 // the group's f tiles are f neighbouring columns, so a half-wave's store covers
 // a whole run of 128 (64 with SwiGLU) outputs.  base (uniform): row 0 of the
@@ -741,20 +651,6 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     }
   }
   wait_vmcnt<0>();  // the dummy stages land before the LDS is given back
-}
-
-// CUs of the current device, a multiple of eight (one share per XCD).
-int workgroups() {
-  static std::atomic<int> cached[64];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
-  int n = cached[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 8) n = 256;
-    n = n / 8 * 8;
-    cached[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
 }
 
 // Row tiles of a dense product of P rows and ntn columns of items.
