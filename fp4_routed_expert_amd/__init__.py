@@ -10,6 +10,9 @@ device memory and streams only.
 
 The operators around the layer (``include/moe_mx4.h``) are in ``mx4``: MXFP4
 quantisation, MXFP4 x MXFP4 products, and the norms before and after a block.
+FP8 with a scale for each block of 128 (``include/moe_fp8_block.h``) is in
+``fp8_block``: quantisation, products, the gated feed-forward block, its backward
+pass and the weight gradient.
 """
 from __future__ import annotations
 
@@ -21,6 +24,11 @@ import torch
 from . import _lib
 from ._lib import (MOE_FLAG_FORCE_DECODE, MOE_FLAG_FORCE_PREFILL, MoeError,  # noqa: F401
                    MoeFp4Weights)
+from .fp8_block import (Fp8BlockWeights, dequant_fp8_block, fp8_block_dense, fp8_block_glu,  # noqa: F401
+                        fp8_block_glu_backward, fp8_block_glu_workspace_size, fp8_block_grouped,
+                        fp8_block_grouped_workspace_size, fp8_block_prepack, fp8_block_prepack_glu,
+                        fp8_block_prepack_t, fp8_block_weight_grad, fp8_block_weight_grad_workspace_size,
+                        quant_fp8_block)
 from .mx4 import (Mxfp4Weights, block_forward, block_workspace_size, dequant_mx, mxfp4_dense,  # noqa: F401
                   mxfp4_grouped, mxfp4_grouped_workspace_size, mxfp4_prepack, mxfp4_prepack_glu,
                   norm_after, norm_before, quant_mxfp4)
@@ -36,6 +44,10 @@ __all__ = [
     "quant_mxfp4", "dequant_mx", "Mxfp4Weights", "mxfp4_prepack", "mxfp4_prepack_glu", "mxfp4_dense",
     "mxfp4_grouped", "mxfp4_grouped_workspace_size", "norm_before", "norm_after", "block_forward",
     "block_workspace_size",
+    "quant_fp8_block", "dequant_fp8_block", "Fp8BlockWeights", "fp8_block_prepack", "fp8_block_prepack_glu",
+    "fp8_block_prepack_t", "fp8_block_dense", "fp8_block_grouped", "fp8_block_grouped_workspace_size",
+    "fp8_block_glu", "fp8_block_glu_backward", "fp8_block_glu_workspace_size", "fp8_block_weight_grad",
+    "fp8_block_weight_grad_workspace_size",
     "MOE_FLAG_FORCE_DECODE", "MOE_FLAG_FORCE_PREFILL", "MoeError",
 ]
 

@@ -30,6 +30,10 @@ MX4_HEADER = os.path.join(os.path.dirname(HERE), "include", "moe_mx4.h")
 MOE_TYPE_BF16, MOE_TYPE_FP16, MOE_TYPE_FP32 = 0, 1, 2
 MOE_QUANT_NONE, MOE_QUANT_MXFP8, MOE_QUANT_MXFP4 = 0, 1, 2
 
+# moe_fp8_block.h
+FP8_BLOCK_HEADER = os.path.join(os.path.dirname(HERE), "include", "moe_fp8_block.h")
+MOE_FP8_BLOCK_LAYOUT_VERSION = 1
+
 
 class MoeFp4Weights(ctypes.Structure):
     _fields_ = [
@@ -64,6 +68,10 @@ class MoeMxfp4Weights(ctypes.Structure):
     ]
 
 
+class MoeFp8BlockWeights(ctypes.Structure):
+    _fields_ = MoeMxfp4Weights._fields_
+
+
 class MoeBlockNorms(ctypes.Structure):
     _fields_ = [
         ("w_pre", ctypes.c_void_p),
@@ -94,6 +102,7 @@ _WP = ctypes.POINTER(MoeFp4Weights)
 _DP = ctypes.POINTER(MoeFp8DenseWeights)
 _MP = ctypes.POINTER(MoeMxfp4Weights)
 _BP = ctypes.POINTER(MoeBlockNorms)
+_FP = ctypes.POINTER(MoeFp8BlockWeights)
 _I64 = ctypes.c_int64
 _F32 = ctypes.c_float
 
@@ -143,6 +152,24 @@ SIGNATURES = {
     "moe_fp4_block_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _U32]),
     "moe_fp4_block_forward": (ctypes.c_int, [_WP, _I32, _P, _BP, _P, _I32, _I32, _I32, _P, _P, _SZ, _U32,
                                              _P]),
+    # moe_fp8_block.h
+    "moe_quant_fp8_block": (ctypes.c_int, [_P, _I32, _I32, _I32, _I64, _P, _P, _P]),
+    "moe_dequant_fp8_block": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _I32, _P]),
+    "moe_fp8_block_packed_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "moe_fp8_block_prepack": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32, _I32, _P, _SZ, _FP, _P]),
+    "moe_fp8_block_prepack_t": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32, _I32, _P, _SZ, _FP, _P]),
+    "moe_fp8_block_dense_forward": (ctypes.c_int, [_FP, _P, _P, _I32, _P, _I32, _U32, _P]),
+    "moe_fp8_block_grouped_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
+    "moe_fp8_block_grouped_forward": (ctypes.c_int, [_FP, _P, _P, _I32, _P, _P, _I32, _I32, _P, _I32, _P, _SZ,
+                                                     _U32, _P]),
+    "moe_fp8_block_glu_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _U32]),
+    "moe_fp8_block_glu_forward": (ctypes.c_int, [_FP, _P, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _SZ,
+                                                 _U32, _P]),
+    "moe_fp8_block_glu_backward": (ctypes.c_int, [_FP, _P, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _SZ,
+                                                  _U32, _P]),
+    "moe_fp8_block_weight_grad_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
+    "moe_fp8_block_weight_grad": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _P,
+                                                 _I32, _P, _SZ, _P]),
 }
 
 

@@ -1,8 +1,9 @@
-// What the files of the C ABI share: the two public headers, the launch
+// What the files of the C ABI share: the public headers, the launch
 // status and the norms' argument checks.
 #pragma once
 
 #include "../../include/moe_fp4.h"
+#include "../../include/moe_fp8_block.h"
 #include "../../include/moe_mx4.h"
 
 namespace moe {

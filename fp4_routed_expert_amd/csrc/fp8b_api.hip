@@ -1,0 +1,267 @@
+// C ABI of the FP8 operators with block scales (declared in
+// include/moe_fp8_block.h): host-side argument checks and path selection.  Every
+// check runs before any launch, so a failing call enqueues nothing and touches no
+// output.
+#include "api.h"
+#include "fp8b.h"
+
+using namespace moe;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+bool known_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_FP16 || t == MOE_TYPE_FP32; }
+bool sum_type(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_FP32; }
+
+constexpr int kMaxE = 1024;
+// A tile past the last row still counts in 32 bits; the streaming product's passes step by next_pass.
+constexpr int kMaxP = INT32_MAX - 256;
+
+// One workgroup of 256 threads per 16 rows and 4 blocks: the grid stays below 2^32 threads in each dimension.
+bool too_many(int32_t M, int32_t K) { return M > kMaxP / 16 * 16 || K > (1 << 20); }
+
+moe_status_t check_enk(int32_t E, int32_t N, int32_t K, int32_t glu) {
+  if (E < 1 || N < 1 || K < 1 || (glu != 0 && glu != 1)) return MOE_ERR_INVALID_ARGUMENT;
+  if (E > kMaxE || N % 32 != 0 || K % 128 != 0 || N > (1 << 20) || K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  // packing runs one thread per 16 bytes and per scale, the latter in one launch dimension
+  if (Fp8bLayout(E, N, K, glu).s_off > (size_t)1 << 42) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t check_weights(const moe_fp8_block_weights_t* w, int32_t glu) {
+  if (!w || !w->packed || w->layout_version != MOE_FP8_BLOCK_LAYOUT_VERSION || w->glu != glu)
+    return MOE_ERR_INVALID_ARGUMENT;
+  const moe_status_t st = check_enk(w->E, w->N, w->K, w->glu);
+  if (st != MOE_OK) return st;
+  if (!aligned(w->packed, 256) || w->packed_bytes < Fp8bLayout(w->E, w->N, w->K, glu != 0).total)
+    return MOE_ERR_INVALID_ARGUMENT;
+  return MOE_OK;
+}
+
+// The tiled product addresses activation rows by 32-bit byte offsets.
+bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 << 32) - 4096; }
+
+// 0: stream the weights, 1: tiled, -1: bad flags.
+constexpr int64_t kStreamRows = 16, kStreamPasses = 1024;
+int choose_path(int64_t P, const Fp8bLayout& L, uint32_t flags) {
+  const bool fd = flags & MOE_FLAG_FORCE_DECODE, fp = flags & MOE_FLAG_FORCE_PREFILL;
+  if ((flags & ~(MOE_FLAG_FORCE_DECODE | MOE_FLAG_FORCE_PREFILL)) != 0 || (fd && fp)) return -1;
+  if (fd) return 0;
+  if (fp) return 1;
+  const int64_t passes = P / 32 + (L.E + 1) / 2;
+  return P <= kStreamRows * L.E || passes * L.NT <= kStreamPasses ? 0 : 1;
+}
+
+size_t tiled_bytes(int32_t P, int32_t E) { return PackedLayout::align256(fp8b_tiled_ws_bytes(P, E)); }
+
+// Workspace of the calls whose rows are quantised: where the weights are streamed, fp32 rows.
+size_t rows_bytes(int32_t P, const Fp8bLayout& L, int path) {
+  return path == 0 ? PackedLayout::align256((size_t)P * L.N * 4) : tiled_bytes(P, L.E);
+}
+
+// One size for the forward and the backward call, which may take different paths (twice the tiles with gate and up).
+size_t glu_bytes(int32_t P, int32_t E, int32_t N, int32_t K, uint32_t flags) {
+  const Fp8bLayout one(E, N, K, false), two(E, N, K, true);
+  const int p1 = choose_path(P, one, flags), p2 = choose_path(P, two, flags);
+  if (p1 < 0 || p2 < 0) return 0;
+  const size_t a = rows_bytes(P, one, p1), b = rows_bytes(P, two, p2);
+  return a > b ? a : b;
+}
+
+// What the grouped calls share: rows and offsets.
+moe_status_t check_rows(int32_t X, const int32_t* offsets, const int32_t* rows, int32_t P, int32_t E) {
+  if (X < 1 || (!rows && X < P)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!offsets && (E != 1 || rows)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(offsets, 4) || !aligned(rows, 4)) return MOE_ERR_INVALID_ARGUMENT;
+  return MOE_OK;
+}
+
+moe_status_t run(const Fp8bArgs& a, const Fp8bLayout& L, int path, Fp8bOut out, void* ws, hipStream_t stream) {
+  return hip_status(path == 0 ? launch_fp8b_stream(a, L, out, static_cast<float*>(ws), stream)
+                              : launch_fp8b_tiled(a, L, out, ws, stream));
+}
+
+moe_status_t prepack(const uint8_t* wq, const float* ws, const uint8_t* uq, const float* us, int32_t E, int32_t N,
+                     int32_t K, bool transposed, void* packed, size_t packed_bytes, moe_fp8_block_weights_t* desc,
+                     hipStream_t stream) {
+  const int32_t glu = uq != nullptr && !transposed;
+  moe_status_t st = check_enk(E, N, K, glu);
+  if (st != MOE_OK) return st;
+  if (transposed && (N % 128 != 0 || (uq && K % 256 != 0))) return MOE_ERR_UNSUPPORTED;
+  if (!wq || !ws || (uq == nullptr) != (us == nullptr) || !packed || !desc) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(wq, 16) || !aligned(uq, 16) || !aligned(ws, 4) || !aligned(us, 4) || !aligned(packed, 256))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const Fp8bLayout L(E, N, K, glu != 0);
+  if (packed_bytes < L.total) return MOE_ERR_INVALID_ARGUMENT;
+  st = hip_status(launch_fp8b_pack(wq, ws, uq, us, L, transposed, static_cast<uint8_t*>(packed), stream));
+  if (st != MOE_OK) return st;
+  desc->E = E;
+  desc->N = N;
+  desc->K = K;
+  desc->glu = glu;
+  desc->layout_version = MOE_FP8_BLOCK_LAYOUT_VERSION;
+  desc->packed = packed;
+  desc->packed_bytes = packed_bytes;
+  return MOE_OK;
+}
+
+// moe_fp8_block_glu_forward and moe_fp8_block_glu_backward
+moe_status_t gated(const moe_fp8_block_weights_t* w, Fp8bOut out, const uint8_t* xq, const float* xs, int32_t X,
+                   const int32_t* offsets, const int32_t* rows, int32_t row_div, int32_t P, uint8_t* q, float* s,
+                   uint16_t* gate, uint16_t* up, void* workspace, size_t workspace_bytes, uint32_t flags,
+                   hipStream_t stream) {
+  const bool grad = out == Fp8bOut::kGluGrad;
+  moe_status_t st = check_weights(w, grad ? 0 : 1);
+  if (st != MOE_OK) return st;
+  if (P < 0 || X < 0 || row_div < 1) return MOE_ERR_INVALID_ARGUMENT;
+  const Fp8bLayout L(w->E, w->N, w->K, w->glu != 0);
+  const int path = choose_path(P, L, flags);
+  if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (w->N % 128 != 0 || rows_too_large(X, w->K) || P > kMaxP) return MOE_ERR_UNSUPPORTED;
+  if (P == 0) return MOE_OK;
+  st = check_rows(X, offsets, rows, P, w->E);
+  if (st != MOE_OK) return st;
+  if (!xq || !xs || !q || !s || (gate == nullptr) != (up == nullptr) || (grad && !gate)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(q, 8) || !aligned(s, 4) || !aligned(gate, 16) || !aligned(up, 16))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!workspace || workspace_bytes < glu_bytes(P, w->E, w->N, w->K, flags)) return MOE_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  const Fp8bArgs a{static_cast<const uint8_t*>(w->packed), xq, xs, X, offsets, rows, row_div, P, nullptr, q, s, gate, up};
+  return run(a, L, path, out, workspace, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_quant_fp8_block(const void* x, int32_t x_type, int32_t M, int32_t K, int64_t ldx, uint8_t* q, float* s,
+                                 hipStream_t stream) {
+  if (M < 0 || K < 1 || ldx < K || !known_type(x_type)) return MOE_ERR_INVALID_ARGUMENT;
+  if (K % 128 != 0 || too_many(M, K)) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !q || !s || !aligned(x, 16) || !aligned(q, 8) || !aligned(s, 4)) return MOE_ERR_INVALID_ARGUMENT;
+  if (M > 1 && ldx % (x_type == MOE_TYPE_FP32 ? 4 : 8) != 0) return MOE_ERR_INVALID_ARGUMENT;
+  return hip_status(launch_fp8b_quant(x, (ElemType)x_type, M, K, M == 1 ? K : (long)ldx, q, s, stream));
+}
+
+moe_status_t moe_dequant_fp8_block(const uint8_t* q, const float* s, int32_t M, int32_t K, void* out, int32_t out_type,
+                                   hipStream_t stream) {
+  if (M < 0 || K < 1 || !known_type(out_type)) return MOE_ERR_INVALID_ARGUMENT;
+  if (K % 128 != 0 || too_many(M, K)) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!q || !s || !out || !aligned(q, 8) || !aligned(s, 4) || !aligned(out, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  return hip_status(launch_fp8b_dequant(q, s, M, K, out, (ElemType)out_type, stream));
+}
+
+size_t moe_fp8_block_packed_bytes(int32_t E, int32_t N, int32_t K, int32_t glu) {
+  if (check_enk(E, N, K, glu) != MOE_OK) return 0;
+  return Fp8bLayout(E, N, K, glu != 0).total;
+}
+
+moe_status_t moe_fp8_block_prepack(const uint8_t* wq, const float* ws, const uint8_t* uq, const float* us, int32_t E,
+                                   int32_t N, int32_t K, void* packed, size_t packed_bytes,
+                                   moe_fp8_block_weights_t* desc, hipStream_t stream) {
+  return prepack(wq, ws, uq, us, E, N, K, false, packed, packed_bytes, desc, stream);
+}
+
+moe_status_t moe_fp8_block_prepack_t(const uint8_t* wq, const float* ws, const uint8_t* uq, const float* us, int32_t E,
+                                     int32_t N, int32_t K, void* packed, size_t packed_bytes,
+                                     moe_fp8_block_weights_t* desc, hipStream_t stream) {
+  return prepack(wq, ws, uq, us, E, N, K, true, packed, packed_bytes, desc, stream);
+}
+
+moe_status_t moe_fp8_block_dense_forward(const moe_fp8_block_weights_t* w, const uint8_t* xq, const float* xs, int32_t T,
+                                         void* y, int32_t y_type, uint32_t flags, hipStream_t stream) {
+  moe_status_t st = check_weights(w, 0);
+  if (st != MOE_OK) return st;
+  if (w->E != 1 || T < 0 || !sum_type(y_type)) return MOE_ERR_INVALID_ARGUMENT;
+  const Fp8bLayout L(1, w->N, w->K, false);
+  const int path = choose_path(T, L, flags);
+  if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows_too_large(T, w->K) || T > kMaxP) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!xq || !xs || !y || !aligned(xq, 16) || !aligned(xs, 4) || !aligned(y, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  const Fp8bArgs a{static_cast<const uint8_t*>(w->packed), xq, xs, T, nullptr, nullptr, 1, T, y, nullptr, nullptr,
+                   nullptr, nullptr};
+  return run(a, L, path, y_type == MOE_TYPE_FP32 ? Fp8bOut::kFp32 : Fp8bOut::kBf16, nullptr, stream);
+}
+
+size_t moe_fp8_block_grouped_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K) {
+  if (P < 0 || P > kMaxP || check_enk(E, N, K, 0) != MOE_OK) return 0;
+  return tiled_bytes(P, E);
+}
+
+moe_status_t moe_fp8_block_grouped_forward(const moe_fp8_block_weights_t* w, const uint8_t* xq, const float* xs,
+                                           int32_t X, const int32_t* offsets, const int32_t* rows, int32_t row_div,
+                                           int32_t P, void* y, int32_t y_type, void* workspace, size_t workspace_bytes,
+                                           uint32_t flags, hipStream_t stream) {
+  moe_status_t st = check_weights(w, 0);
+  if (st != MOE_OK) return st;
+  if (P < 0 || X < 0 || row_div < 1 || !sum_type(y_type)) return MOE_ERR_INVALID_ARGUMENT;
+  const Fp8bLayout L(w->E, w->N, w->K, false);
+  const int path = choose_path(P, L, flags);
+  if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows_too_large(X, w->K) || P > kMaxP) return MOE_ERR_UNSUPPORTED;
+  if (P == 0) return MOE_OK;
+  if (!offsets) return MOE_ERR_INVALID_ARGUMENT;
+  st = check_rows(X, offsets, rows, P, w->E);
+  if (st != MOE_OK) return st;
+  if (!xq || !xs || !y || !aligned(xq, 16) || !aligned(xs, 4) || !aligned(y, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!workspace || workspace_bytes < tiled_bytes(P, w->E)) return MOE_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  const Fp8bArgs a{static_cast<const uint8_t*>(w->packed), xq, xs, X, offsets, rows, row_div, P, y, nullptr, nullptr,
+                   nullptr, nullptr};
+  return run(a, L, path, y_type == MOE_TYPE_FP32 ? Fp8bOut::kFp32 : Fp8bOut::kBf16, workspace, stream);
+}
+
+size_t moe_fp8_block_glu_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K, uint32_t flags) {
+  if (P < 0 || P > kMaxP || check_enk(E, N, K, 0) != MOE_OK) return 0;
+  return glu_bytes(P, E, N, K, flags);
+}
+
+moe_status_t moe_fp8_block_glu_forward(const moe_fp8_block_weights_t* w, const uint8_t* xq, const float* xs, int32_t X,
+                                       const int32_t* offsets, const int32_t* rows, int32_t row_div, int32_t P,
+                                       uint8_t* q, float* s, uint16_t* gate, uint16_t* up, void* workspace,
+                                       size_t workspace_bytes, uint32_t flags, hipStream_t stream) {
+  return gated(w, Fp8bOut::kGlu, xq, xs, X, offsets, rows, row_div, P, q, s, gate, up, workspace, workspace_bytes, flags,
+               stream);
+}
+
+moe_status_t moe_fp8_block_glu_backward(const moe_fp8_block_weights_t* w, const uint8_t* yq, const float* ys, int32_t X,
+                                        const int32_t* offsets, const int32_t* rows, int32_t row_div, int32_t P,
+                                        const uint16_t* gate, const uint16_t* up, uint8_t* q, float* s, void* workspace,
+                                        size_t workspace_bytes, uint32_t flags, hipStream_t stream) {
+  return gated(w, Fp8bOut::kGluGrad, yq, ys, X, offsets, rows, row_div, P, q, s, const_cast<uint16_t*>(gate),
+               const_cast<uint16_t*>(up), workspace, workspace_bytes, flags, stream);
+}
+
+size_t moe_fp8_block_weight_grad_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K) {
+  if (P < 0 || P > kMaxP || check_enk(E, N, K, 0) != MOE_OK || N % 128 != 0) return 0;
+  return PackedLayout::align256(fp8b_grad_ws_bytes(P, E, N, K));
+}
+
+moe_status_t moe_fp8_block_weight_grad(const uint8_t* yq, const float* ys, const uint8_t* xq, const float* xs, int32_t X,
+                                       const int32_t* offsets, const int32_t* rows, int32_t row_div, int32_t P,
+                                       int32_t E, int32_t N, int32_t K, void* dw, int32_t dw_type, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream) {
+  moe_status_t st = check_enk(E, N, K, 0);
+  if (st != MOE_OK) return st;
+  if (P < 0 || X < 0 || row_div < 1 || !sum_type(dw_type)) return MOE_ERR_INVALID_ARGUMENT;
+  // (one workgroup of 512 threads per 256 x 256 outputs, below 2^32 threads)
+  if (N % 128 != 0 || P > kMaxP || (int64_t)N * K >= (int64_t)1 << 39) return MOE_ERR_UNSUPPORTED;
+  if (!dw || !aligned(dw, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  if (P > 0) {
+    st = check_rows(X, offsets, rows, P, E);
+    if (st != MOE_OK) return st;
+    if (!yq || !ys || !xq || !xs || !aligned(yq, 16) || !aligned(xq, 16) || !aligned(ys, 4) || !aligned(xs, 4))
+      return MOE_ERR_INVALID_ARGUMENT;
+  }
+  const size_t need = PackedLayout::align256(fp8b_grad_ws_bytes(P, E, N, K));
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  // without rows nothing is read: dw is zeros
+  const Fp8bGradArgs a{yq, ys, xq, xs, X, P > 0 ? offsets : nullptr, rows, row_div, P, E, N, K, dw};
+  return hip_status(launch_fp8b_grad(a, dw_type == MOE_TYPE_FP32, workspace, stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,221 @@
+// FP8 products with block scales of 128 for few rows: y[s, n] = sum over blocks
+// b of sx[b, r] sw[n / 128, b] (sum_{k in b} xq[r, k] wq[e, n, k]).  One MFMA
+// (K = 128) is one block's sum; the two scales meet it in one fp32 multiply-add
+// per element, since they are no powers of two.
+//
+// Weight streaming, bound by HBM: a workgroup owns two neighbouring weight
+// tiles (32 columns, or 16 columns of gate and up) of one expert, or one tile
+// where there are few, and 16 or 32 of its token rows at a time; its waves take
+// the K-steps in turn, so that at any moment they read neighbouring 2 KiB blocks
+// of each tile, kB steps in flight per wave, and their sums are joined through
+// LDS in wave order (the same inputs give the same bits).
+#include "fp8b.h"
+
+namespace moe {
+namespace {
+
+template <int NT, int TT>
+struct Step {
+  v4u w[NT][2], x[TT][2];
+  float sw[NT], sx[TT];
+};
+
+// What one pass reads: this lane's bytes of each tile and token row at K-step 0.
+template <int NT, int TT>
+struct Source {
+  const uint8_t* w[NT];
+  const float* sw[NT];  // uniform
+  const uint8_t* x[TT];
+  const float* sx[TT];
+  long X;  // floats from a block's row scales to the next one's
+};
+
+template <int NT, int TT>
+__device__ __forceinline__ void load_step(Step<NT, TT>& p, const Source<NT, TT>& s, int j) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    // weights are read once: non-temporal loads leave the caches to the rows
+    const uint8_t* w = s.w[t] + (size_t)j * 2048;
+    p.w[t][0] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(w));
+    p.w[t][1] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(w + 1024));
+    p.sw[t] = s.sw[t][j];
+  }
+#pragma unroll
+  for (int i = 0; i < TT; ++i) {
+    p.x[i][0] = *reinterpret_cast<const v4u*>(s.x[i] + (size_t)j * 128);
+    p.x[i][1] = *reinterpret_cast<const v4u*>(s.x[i] + (size_t)j * 128 + 64);
+    p.sx[i] = s.sx[i][(size_t)j * s.X];
+  }
+}
+
+template <int NT, int TT>
+__device__ __forceinline__ void multiply(const Step<NT, TT>& p, v4f (&acc)[NT][TT]) {
+  v4f d[NT][TT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+      d[t][i] = mfma_block(cat_pieces(p.w[t][0], p.w[t][1]), cat_pieces(p.x[i][0], p.x[i][1]));
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const float k = p.sx[i] * p.sw[t];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[t][i][v] = fmaf(d[t][i][v], k, acc[t][i][v]);
+    }
+}
+
+// kOut: kBf16 and kFp32 write a.y; kGlu writes h to a.y as fp32 rows, and gate
+// and up where they are wanted.
+template <int NW, int NT, int TT, int kB, Fp8bOut kOut>
+__global__ __launch_bounds__(64 * NW) void stream_kernel(Fp8bArgs a, Fp8bLayout L) {
+  constexpr bool kGlu = kOut == Fp8bOut::kGlu;
+  static_assert(NT == 2 || (NT == 1 && !kGlu), "a gate tile with its up tile");
+  constexpr int kRows = 16 * TT;
+  __shared__ v4f red[NW][NT * TT][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int nt0 = blockIdx.x * NT;
+  const int J = L.J;
+  int e, begin, end, stride;
+  if (a.offsets) {
+    // offsets come from device memory: kept inside the rows of y whatever they hold
+    e = blockIdx.y;
+    begin = min(max(a.offsets[e], 0), a.P);
+    end = min(max(a.offsets[e + 1], begin), a.P);
+    if ((int)blockIdx.z >= (end - begin + kRows - 1) / kRows) return;  // uniform: before any barrier
+    begin += blockIdx.z * kRows;
+    stride = kRows * gridDim.z;
+  } else {
+    e = 0;
+    begin = blockIdx.y * kRows;
+    end = a.P;
+    stride = kRows * gridDim.y;
+  }
+  Source<NT, TT> src;
+  src.X = a.X;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    src.w[t] = a.packed + L.tile_off(e, nt0 + t) + 16 * lane;
+    // row block: of the pair's 16 columns with gate and up, else of the tile's pair
+    const int b = kGlu ? 2 * (nt0 >> 4) + t : (nt0 + t) >> 3;
+    src.sw[t] = reinterpret_cast<const float*>(a.packed + L.s_off) + ((size_t)e * L.NB + b) * J;
+  }
+  const int nsteps = J > wave ? (J - wave + NW - 1) / NW : 0;
+  for (int m0 = begin; m0 < end; m0 = next_pass(m0, stride, end)) {
+    const int rows = min(kRows, end - m0);
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      int xr = m0 + min(16 * i + r, rows - 1);
+      if (a.rows) xr = entry_row(a.rows, xr, a.div, a.X);
+      src.x[i] = a.xq + (size_t)xr * L.K + 16 * g;
+      src.sx[i] = a.xs + xr;
+    }
+    v4f acc[NT][TT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < TT; ++i) acc[t][i] = v4f{0.f, 0.f, 0.f, 0.f};
+    Step<NT, TT> p[kB];
+    int u = 0;
+    for (; u + kB <= nsteps; u += kB) {
+#pragma unroll
+      for (int b = 0; b < kB; ++b) load_step(p[b], src, wave + NW * (u + b));
+#pragma unroll
+      for (int b = 0; b < kB; ++b) multiply(p[b], acc);
+    }
+    for (; u < nsteps; ++u) {
+      load_step(p[0], src, wave + NW * u);
+      multiply(p[0], acc);
+    }
+    const int nb = (rows + 15) / 16;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
+        if (i < nb) red[wave][NT * i + t][lane] = acc[t][i];
+    __syncthreads();
+    constexpr int kEach = kGlu ? 1 : NT;  // outputs of a token tile
+    for (int o = wave; o < kEach * nb; o += NW) {
+      const int i = o / kEach, t = o % kEach;
+      v4f s = red[0][NT * i + t][lane];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) s += red[w][NT * i + t][lane];
+      v4f up{};
+      if constexpr (kGlu) {
+        up = red[0][NT * i + 1][lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) up += red[w][NT * i + 1][lane];
+      }
+      const int m = 16 * i + r;
+      if (m >= rows) continue;
+      const size_t at = (size_t)(m0 + m) * L.N + L.column(nt0 + t, 4 * g);
+      if constexpr (kGlu) {
+        if (a.gate) {
+          *reinterpret_cast<uint2*>(a.gate + at) = make_uint2(f32x2_to_bf16(s[0], s[1]), f32x2_to_bf16(s[2], s[3]));
+          *reinterpret_cast<uint2*>(a.up + at) = make_uint2(f32x2_to_bf16(up[0], up[1]), f32x2_to_bf16(up[2], up[3]));
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) s[v] = glu_out(s[v], up[v]);
+      }
+      if constexpr (kOut == Fp8bOut::kBf16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+            make_uint2(f32x2_to_bf16(s[0], s[1]), f32x2_to_bf16(s[2], s[3]));
+      else
+        *reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at) = s;
+    }
+    __syncthreads();  // the sums are read before the next pass writes them
+  }
+}
+
+// Passes over one group's rows that run side by side: one where the groups'
+// tiles alone fill the CUs, more where there are few.
+int passes_at_once(int P, const Fp8bLayout& L, int rows) {
+  return min(max(1536 / (int)min((long)L.E * L.NT, 1536l), 1), max((P + rows - 1) / rows, 1));
+}
+
+template <int NW, int NT, int TT, int kB, Fp8bOut kOut>
+void stream_as(const Fp8bArgs& a, const Fp8bLayout& L, hipStream_t st) {
+  constexpr int kRows = 16 * TT;
+  const dim3 grid((unsigned)(L.NT / NT), a.offsets ? (unsigned)L.E : (unsigned)min((a.P + kRows - 1) / kRows, 65535),
+                  a.offsets ? (unsigned)passes_at_once(a.P, L, kRows) : 1u);
+  hipLaunchKernelGGL((stream_kernel<NW, NT, TT, kB, kOut>), grid, dim3(64 * NW), 0, st, a, L);
+}
+
+template <Fp8bOut kOut>
+void stream_for(const Fp8bArgs& a, const Fp8bLayout& L, hipStream_t st) {
+  constexpr bool kGlu = kOut == Fp8bOut::kGlu;
+  const bool two = a.P > 16 * (a.offsets ? L.E : 1);
+  if (two)
+    stream_as<8, 2, 2, 2, kOut>(a, L, st);
+  else if (kGlu || L.NT > 512)
+    stream_as<8, 2, 1, 2, kOut>(a, L, st);
+  else
+    stream_as<16, kGlu ? 2 : 1, 1, 2, kOut>(a, L, st);
+}
+
+}  // namespace
+
+hipError_t launch_fp8b_stream(const Fp8bArgs& args, const Fp8bLayout& L, Fp8bOut out, float* ws, hipStream_t st) {
+  Fp8bArgs a = args;
+  if (out == Fp8bOut::kBf16) {
+    stream_for<Fp8bOut::kBf16>(a, L, st);
+    return hipGetLastError();
+  }
+  if (out == Fp8bOut::kFp32) {
+    stream_for<Fp8bOut::kFp32>(a, L, st);
+    return hipGetLastError();
+  }
+  // A block of 128 outputs is spread over several workgroups here, so the rows
+  // go through memory as fp32 and are quantised by a second launch.
+  a.y = ws;
+  if (out == Fp8bOut::kGlu)
+    stream_for<Fp8bOut::kGlu>(a, L, st);
+  else
+    stream_for<Fp8bOut::kFp32>(a, L, st);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_fp8b_rows(ws, args, L.E, L.N, out, st);
+}
+
+}  // namespace moe

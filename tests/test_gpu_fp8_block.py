@@ -1,0 +1,440 @@
+"""The FP8 operators with block scales of 128 on the GPU against their definitions in 64 bits."""
+import pytest
+import torch
+
+import fp4_routed_expert_amd as moe
+import fp8b_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEC, PRE = moe.MOE_FLAG_FORCE_DECODE, moe.MOE_FLAG_FORCE_PREFILL
+BF, FH, FS = torch.bfloat16, torch.float16, torch.float32
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def normal(g, *shape):
+    return torch.randn(*shape, device="cuda", generator=g)
+
+
+def make_rows(g, M, K):
+    return ref.quant((normal(g, M, K) * torch.exp(normal(g, M, 1))).to(BF))
+
+
+def make_weights(g, E, N, K):
+    """Codes of every magnitude, scales of every block its own."""
+    q = (normal(g, E, N, K) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    s = torch.exp(normal(g, E, (N + 127) // 128, K // 128)) * K ** -0.5 / 100
+    return q, s
+
+
+def within(got, want, err, what=""):
+    d = (got.double() - want).abs()
+    bad = ~(d <= err)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float((d / err).nan_to_num(9e9).max()):.3g}x"
+
+
+# ------------------------------------------------------------- quantisation
+@pytest.mark.parametrize("dtype", [BF, FH, FS])
+@pytest.mark.parametrize("M,K", [(1, 128), (5, 384), (16, 512), (17, 640), (130, 7168)])
+def test_quant(dtype, M, K):
+    g = gen(M + K)
+    x = (normal(g, M, K) * torch.exp(2 * normal(g, M, 1))).to(dtype)
+    x[0, :128] = 0
+    if M > 4:
+        x[1, 3], x[2, 130], x[3, 1], x[4, 200] = float("nan"), float("inf"), -0.0, float("-inf")
+    q, s = moe.quant_fp8_block(x)
+    wq, ws = ref.quant(x)
+    assert torch.equal(q, wq)
+    assert torch.equal(s.isnan(), ws.isnan()) and torch.equal(s.nan_to_num(0), ws.nan_to_num(0))
+    for out in (BF, FH, FS):
+        v = moe.dequant_fp8_block(q, s, dtype=out)
+        want = (ref.code_values(wq).float() * ws.t().repeat_interleave(128, 1)).to(out)
+        assert torch.equal(v.isnan(), want.isnan()) and torch.equal(v.nan_to_num(0), want.nan_to_num(0))
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -149, 2.0 ** -120, 2.0 ** -100, 2.0 ** 100, 2.0 ** 126])
+def test_quant_ends_of_the_range(scale):
+    x = torch.linspace(-1, 1, 256, device="cuda").view(2, 128) * scale
+    q, s = moe.quant_fp8_block(x)
+    wq, ws = ref.quant(x)
+    assert torch.equal(q, wq) and torch.equal(s, ws)
+
+
+def test_quant_strided_rows_and_views():
+    g = gen(7)
+    x = normal(g, 9, 520).to(BF)[:, 8:264]
+    q, s = moe.quant_fp8_block(x)
+    wq, ws = ref.quant(x)
+    assert torch.equal(q, wq) and torch.equal(s, ws)
+    x = normal(g, 1, 256)
+    assert torch.equal(moe.quant_fp8_block(x)[0], ref.quant(x)[0])
+    q, s = moe.quant_fp8_block(torch.empty(0, 256, device="cuda"))
+    assert q.shape == (0, 256) and s.shape == (2, 0)
+
+
+def test_quant_codes_of_torchs_type():
+    x = normal(gen(8), 4, 256)
+    q = torch.empty(4, 256, dtype=torch.float8_e4m3fn, device="cuda")
+    s = moe.quant_fp8_block(x, q=q)[1]
+    assert torch.equal(q.float() * s.t().repeat_interleave(128, 1), moe.dequant_fp8_block(q, s, dtype=FS))
+
+
+# ------------------------------------------------------------ dense product
+@pytest.mark.parametrize("flags", [DEC, PRE])
+@pytest.mark.parametrize("dtype", [BF, FS])
+@pytest.mark.parametrize("T,K,N", [(1, 128, 32), (3, 256, 160), (16, 384, 128), (17, 128, 288), (40, 1024, 256),
+                                   (257, 640, 352), (600, 256, 512)])
+def test_dense(flags, dtype, T, K, N):
+    g = gen(T * 7 + K + N)
+    xq, xs = make_rows(g, T, K)
+    wq, ws = make_weights(g, 1, N, K)
+    w = moe.fp8_block_prepack(wq[0], ws[0])
+    y = torch.full((T + 1, N), 7.0, dtype=dtype, device="cuda")
+    moe.fp8_block_dense(w, xq, xs, flags=flags, y=y[:T])
+    want, err = ref.product(ref.rows(xq, xs), ref.weights(wq[0], ws[0]), ref.HALF[dtype])
+    within(y[:T], want, err)
+    assert (y[T] == 7).all()
+    assert torch.equal(moe.fp8_block_dense(w, xq, xs, flags=flags, dtype=dtype), y[:T])
+
+
+@pytest.mark.parametrize("flags", [DEC, PRE])
+def test_dense_nan_stays_in_its_row(flags):
+    g = gen(3)
+    x = normal(g, 20, 256).to(BF)
+    x[4, 200] = float("nan")
+    xq, xs = moe.quant_fp8_block(x)
+    wq, ws = make_weights(g, 1, 64, 256)
+    y = moe.fp8_block_dense(moe.fp8_block_prepack(wq[0], ws[0]), xq, xs, flags=flags)
+    bad = y.isnan()
+    assert bad[4].all() and not bad[:4].any() and not bad[5:].any()
+
+
+@pytest.mark.parametrize("flags", [DEC, PRE])
+def test_dense_nan_weight_stays_in_its_column(flags):
+    g = gen(4)
+    xq, xs = make_rows(g, 20, 256)
+    wq, ws = make_weights(g, 1, 64, 256)
+    wq[0, 37, 140] = 0x7F
+    y = moe.fp8_block_dense(moe.fp8_block_prepack(wq[0], ws[0]), xq, xs, flags=flags)
+    bad = y.isnan()
+    assert bad[:, 37].all() and int(bad.sum()) == 20
+
+
+def test_dense_transposed_weights():
+    g = gen(11)
+    xq, xs = make_rows(g, 33, 512)
+    wq, ws = make_weights(g, 2, 256, 384)
+    for pair, K in ((False, 256), (True, 512)):
+        w = (moe.fp8_block_prepack_t(wq[0], ws[0], wq[1], ws[1]) if pair else moe.fp8_block_prepack_t(wq[0], ws[0]))
+        full = torch.cat([ref.weights(wq[0], ws[0]), ref.weights(wq[1], ws[1])])[:K]
+        y = moe.fp8_block_dense(w, xq[:, :K].contiguous(), xs[:K // 128].contiguous(), dtype=FS)
+        want, err = ref.product(ref.rows(xq, xs)[:, :K], full.T.contiguous())
+        within(y, want, err)
+
+
+# ---------------------------------------------------------- grouped product
+# sizes of the groups (0: no rows), rows in front of and behind them
+GROUPS = {"one each": ([1, 1, 1], 0, 0), "ragged": ([0, 17, 1, 0, 40, 16, 0], 0, 0), "left alone": ([5, 0, 33], 3, 4),
+          "large": ([300, 0, 70, 513], 0, 9), "all in one": ([0, 0, 260], 1, 0), "none": ([0, 0], 2, 3)}
+
+
+def grouping(name, k=1, seed=0):
+    """offsets, the pair of each row (in a random order of X = rows / k tokens), the expert of each row or -1."""
+    sizes, front, back = GROUPS[name]
+    P = front + sum(sizes) + back
+    P = (P + k - 1) // k * k
+    off = torch.tensor([front] + sizes).cumsum(0).int().cuda()
+    expert = torch.full((P,), -1)
+    at = front
+    for e, n in enumerate(sizes):
+        expert[at:at + n] = e
+        at += n
+    pair = torch.randperm(P, generator=torch.Generator().manual_seed(seed)).int().cuda()
+    return off, pair, expert.cuda(), P, len(sizes)
+
+
+@pytest.mark.parametrize("flags", [DEC, PRE])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("name", list(GROUPS))
+@pytest.mark.parametrize("K,N,dtype", [(128, 32, FS), (640, 416, BF)])
+def test_grouped(flags, gather, name, K, N, dtype):
+    k = 2 if gather else 1
+    off, pair, expert, P, E = grouping(name, k)
+    g = gen(P + K)
+    xq, xs = make_rows(g, P // k, K)
+    wq, ws = make_weights(g, E, N, K)
+    y = torch.full((P, N), 7.0, dtype=dtype, device="cuda")
+    w = moe.fp8_block_prepack(wq, ws)
+    moe.fp8_block_grouped(w, xq, xs, off, **({"rows": pair, "row_div": k} if gather else {}), flags=flags, y=y)
+    x = ref.rows(xq, xs)
+    if gather:
+        x = x[(pair // k).long()]
+    assert (y[expert < 0] == 7).all()
+    for e in range(E):
+        at = expert == e
+        want, err = ref.product(x[at], ref.weights(wq[e], ws[e]), ref.HALF[dtype])
+        within(y[at], want, err, f"expert {e}")
+
+
+def test_grouped_offsets_and_rows_out_of_range_stay_inside():
+    g = gen(5)
+    xq, xs = make_rows(g, 40, 256)
+    wq, ws = make_weights(g, 3, 64, 256)
+    w = moe.fp8_block_prepack(wq, ws)
+    y = torch.zeros(48, 64, device="cuda")
+    off = torch.tensor([-4, 10, 1 << 30, (1 << 31) - 1], dtype=torch.int32, device="cuda")
+    rows = torch.arange(40, device="cuda", dtype=torch.int32)
+    rows[3], rows[20] = 1 << 30, -5
+    for flags in (DEC, PRE):
+        y.fill_(7)
+        moe.fp8_block_grouped(w, xq, xs, off, rows=rows, flags=flags, y=y[:40])
+        assert (y[40:] == 7).all()
+        r = rows.long().where((rows >= 0) & (rows < 40), torch.tensor(39, device="cuda"))
+        x = ref.rows(xq, xs)[r]
+        for e, a, b in ((0, 0, 10), (1, 10, 40)):
+            want, err = ref.product(x[a:b], ref.weights(wq[e], ws[e]))
+            within(y[a:b], want, err)
+
+
+# ------------------------------------------------- gated feed-forward block
+@pytest.mark.parametrize("flags", [DEC, PRE])
+@pytest.mark.parametrize("name", ["ragged", "left alone", "large", "none"])
+@pytest.mark.parametrize("K,N,save", [(128, 128, True), (768, 384, False), (256, 640, True)])
+def test_glu(flags, name, K, N, save):
+    k = 2
+    off, pair, expert, P, E = grouping(name, k)
+    g = gen(P + N)
+    xq, xs = make_rows(g, P // k, K)
+    (wq, ws), (uq, us) = make_weights(g, E, N, K), make_weights(g, E, N, K)
+    q, s = torch.full((P, N), 9, dtype=torch.uint8, device="cuda"), torch.full((N // 128, P), 7.0, device="cuda")
+    gate, up = (torch.full((P, N), 7.0, dtype=BF, device="cuda") for _ in range(2)) if save else (None, None)
+    moe.fp8_block_glu(moe.fp8_block_prepack_glu(wq, ws, uq, us), xq, xs, off, rows=pair, row_div=k, flags=flags, q=q,
+                      s=s, gate=gate, up=up)
+    out = expert < 0
+    assert (q[out] == 9).all() and (s[:, out] == 7).all()
+    x = ref.rows(xq, xs)[(pair // k).long()]
+    for e in range(E):
+        at = expert == e
+        (a, ea), (b, eb), (h, eh) = ref.glu(x[at], ref.weights(wq[e], ws[e]), ref.weights(uq[e], us[e]))
+        if at.any():
+            within(ref.rows(q[at], s[:, at]), h, ref.held(h, eh), f"expert {e}")
+        if save:
+            within(gate[at], a, ea + ref.HALF[BF] * (a.abs() + ea), "gate")
+            within(up[at], b, eb + ref.HALF[BF] * (b.abs() + eb), "up")
+    if save:
+        assert (gate[out] == 7).all() and (up[out] == 7).all()
+
+
+@pytest.mark.parametrize("flags", [DEC, PRE])
+@pytest.mark.parametrize("T", [1, 20, 300])
+def test_glu_without_groups(flags, T):
+    g = gen(T)
+    xq, xs = make_rows(g, T, 384)
+    (wq, ws), (uq, us) = make_weights(g, 1, 256, 384), make_weights(g, 1, 256, 384)
+    q, s, gate, up = moe.fp8_block_glu(moe.fp8_block_prepack_glu(wq[0], ws[0], uq[0], us[0]), xq, xs, flags=flags)
+    assert gate is None and up is None
+    _, _, (h, eh) = ref.glu(ref.rows(xq, xs), ref.weights(wq[0], ws[0]), ref.weights(uq[0], us[0]))
+    within(ref.rows(q, s), h, ref.held(h, eh))
+
+
+@pytest.mark.parametrize("flags", [DEC, PRE])
+def test_glu_closed_gates_and_bad_rows(flags):
+    """Gates far below zero close; a NaN row is NaN, its neighbours are not."""
+    g = gen(2)
+    x = normal(g, 18, 128).to(BF)
+    x[5, 0] = float("inf")
+    xq, xs = moe.quant_fp8_block(x)
+    wq = torch.full((1, 128, 128), 0x7E, dtype=torch.uint8, device="cuda")  # 448
+    ws = torch.ones(1, 1, 1, device="cuda")
+    uq, us = make_weights(g, 1, 128, 128)
+    q, s, gate, up = moe.fp8_block_glu(moe.fp8_block_prepack_glu(wq, ws, uq, us), xq, xs, flags=flags, save=True)
+    v = ref.rows(q, s)
+    assert s[0, 5].isnan() and (q[5] == 0).all() and int(s.isnan().sum()) == 1
+    for i in range(18):
+        if i != 5 and gate[i, 0] < -100:
+            assert (v[i] == 0).all()
+        elif i != 5:
+            assert v[i].isfinite().all()
+
+
+# ------------------------------------------------------------ backward pass
+@pytest.mark.parametrize("flags", [DEC, PRE])
+@pytest.mark.parametrize("name", ["ragged", "left alone", "large", "none"])
+@pytest.mark.parametrize("K,N", [(128, 128), (256, 384), (640, 256)])
+def test_glu_backward(flags, name, K, N):
+    off, _, expert, P, E = grouping(name)
+    g = gen(P + K)
+    yq, ys = make_rows(g, P, K)
+    wq, ws = make_weights(g, E, K, N)
+    gate, up = (4 * normal(g, P, N)).to(BF), normal(g, P, N).to(BF)
+    q, s = torch.full((P, 2 * N), 9, dtype=torch.uint8, device="cuda"), torch.full((2 * N // 128, P), 7.0, device="cuda")
+    moe.fp8_block_glu_backward(moe.fp8_block_prepack_t(wq, ws), yq, ys, gate, up, off, flags=flags, q=q, s=s)
+    out = expert < 0
+    assert (q[out] == 9).all() and (s[:, out] == 7).all()
+    dy = ref.rows(yq, ys)
+    for e in range(E):
+        at = expert == e
+        if not at.any():
+            continue
+        dh, adh = ref.product(dy[at], ref.weights(wq[e], ws[e]).T.contiguous())
+        (dg, ag), (du, au) = ref.glu_grad(dh, adh, gate[at].double(), up[at].double())
+        v = ref.rows(q[at], s[:, at])
+        within(v[:, :N], dg, ref.held(dg, ag), f"dg, expert {e}")
+        within(v[:, N:], du, ref.held(du, au), f"du, expert {e}")
+
+
+def test_glu_grad_against_differences():
+    """The formula that the kernel is tested against is the derivative of silu(g) u."""
+    g, u = torch.linspace(-6, 6, 49, dtype=torch.float64), torch.linspace(2, -3, 49, dtype=torch.float64)
+    one = torch.ones_like(g)
+    (dg, _), (du, _) = ref.glu_grad(one, 0 * one, g, u)
+    f = lambda a, b: a * torch.sigmoid(a) * b  # noqa: E731
+    d = 1e-5
+    assert ((f(g + d, u) - f(g - d, u)) / (2 * d) - dg).abs().max() < 1e-8
+    assert ((f(g, u + d) - f(g, u - d)) / (2 * d) - du).abs().max() < 1e-8
+
+
+def grad_bound(y, x, half):
+    """dw, and its largest error: dy times both scales is rounded to bf16 once (half a step of a value in [1, 2) is
+    2^-8: eight significant bits), behind two fp32 roundings; the sum of n products in fp32."""
+    n = y.shape[0]
+    want, mags = y.T.contiguous() @ x, y.abs().T.contiguous() @ x.abs()
+    a = (ref.HALF[BF] * (1 + 2.0 ** -22) + ref.gamma(n)) * mags
+    return want, a + half * (want.abs() + a)
+
+
+@pytest.mark.parametrize("dtype", [BF, FS])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("name", list(GROUPS))
+@pytest.mark.parametrize("N,K", [(128, 128), (384, 256), (256, 640)])
+def test_weight_grad(dtype, gather, name, N, K):
+    k = 2 if gather else 1
+    off, pair, expert, P, E = grouping(name, k)
+    g = gen(P + N)
+    yq, ys = make_rows(g, P, N)
+    xq, xs = make_rows(g, P // k, K)
+    dw = moe.fp8_block_weight_grad(yq, ys, xq, xs, off, **({"rows": pair, "row_div": k} if gather else {}), dtype=dtype)
+    y, x = ref.rows(yq, ys), ref.rows(xq, xs)
+    if gather:
+        x = x[(pair // k).long()]
+    for e in range(E):
+        at = expert == e
+        want, err = grad_bound(y[at], x[at], ref.HALF[dtype])
+        within(dw[e], want, err + 1e-300, f"expert {e}")
+
+
+@pytest.mark.parametrize("T", [0, 1, 33, 700, 2100])
+@pytest.mark.parametrize("dtype", [BF, FS])
+def test_weight_grad_of_one_group(T, dtype):
+    """Few tiles: the rows are split and their sums joined."""
+    g = gen(T)
+    yq, ys = make_rows(g, T, 256)
+    xq, xs = make_rows(g, T, 128)
+    dw = moe.fp8_block_weight_grad(yq, ys, xq, xs, dtype=dtype)
+    want, err = grad_bound(ref.rows(yq, ys), ref.rows(xq, xs), ref.HALF[dtype])
+    assert dw.shape == (256, 128)
+    within(dw, want, err + 1e-300)
+    assert torch.equal(dw, moe.fp8_block_weight_grad(yq, ys, xq, xs, dtype=dtype))
+
+
+def test_weight_grad_nan_row_stays_in_its_group():
+    off, _, expert, P, E = grouping("ragged")
+    g = gen(1)
+    x = normal(g, P, 128)
+    x[int(off[4]), 3] = float("nan")
+    yq, ys = make_rows(g, P, 128)
+    dw = moe.fp8_block_weight_grad(yq, ys, *moe.quant_fp8_block(x), off)
+    assert dw[4].isnan().any() and not dw[:4].isnan().any() and not dw[5:].isnan().any()
+
+
+# ------------------------------------------------------------- as it is used
+def feed_forward(w, x, do, off, pair, k, ws=None):
+    """One expert layer's forward and backward pass as a program makes them."""
+    xq, xs = moe.quant_fp8_block(x)
+    hq, hs, gate, up = moe.fp8_block_glu(w["w13"], xq, xs, off, rows=pair, row_div=k, save=True)
+    o = moe.fp8_block_grouped(w["w2"], hq, hs, off)
+    dq, ds = moe.quant_fp8_block(do)
+    gq, gs = moe.fp8_block_glu_backward(w["w2_t"], dq, ds, gate, up, off)
+    dx = moe.fp8_block_grouped(w["w13_t"], gq, gs, off, dtype=FS)
+    dw2 = moe.fp8_block_weight_grad(dq, ds, hq, hs, off)
+    dw13 = moe.fp8_block_weight_grad(gq, gs, xq, xs, off, rows=pair, row_div=k)
+    return o, dx, dw2, dw13
+
+
+def training_case(T=70, k=2, E=5, H=256, I=128, seed=0):
+    g = gen(seed)
+    x = normal(g, T, H).to(BF)
+    ids, _ = moe.route_topk(normal(g, T, E), k)
+    _, off, pair, pos = moe.sort_permute(ids, E)
+    m = {n: make_weights(g, E, *s) for n, s in (("w1", (I, H)), ("w3", (I, H)), ("w2", (H, I)))}
+    w = {"w13": moe.fp8_block_prepack_glu(*m["w1"], *m["w3"]), "w2": moe.fp8_block_prepack(*m["w2"]),
+         "w2_t": moe.fp8_block_prepack_t(*m["w2"]), "w13_t": moe.fp8_block_prepack_t(*m["w1"], *m["w3"])}
+    return w, m, x, normal(g, T * k, H).to(BF), off, pair, k, E
+
+
+@pytest.mark.parametrize("T", [3, 70, 400])
+def test_forward_and_backward_chain(T):
+    """The chain's results against the unquantised layer's in 64 bits: what e4m3 rounds (a step of 2^-4 relative at
+    most, 2^-5 on average of a binade's values) enters twice in each result's factors, so norms agree to a tenth."""
+    w, m, x, do, off, pair, k, E = training_case(T)
+    got = feed_forward(w, x, do, off, pair, k)
+    v = {n: ref.weights(*m[n]).requires_grad_() for n in m}
+    xd = x.double()[(pair // k).long()].requires_grad_()
+    parts = []
+    for e in range(E):
+        a = xd[int(off[e]):int(off[e + 1])]
+        gate = a @ v["w1"][e].T
+        parts.append((gate * torch.sigmoid(gate) * (a @ v["w3"][e].T)) @ v["w2"][e].T)
+    o = torch.cat(parts)
+    o.backward(do.double())
+    want = (o.detach(), xd.grad, v["w2"].grad, torch.cat([v["w1"].grad, v["w3"].grad], 1))
+    for a, b, what in zip(got, want, ("o", "dx", "dw2", "dw13")):
+        assert (a.double() - b).norm() < 0.1 * b.norm(), what
+
+
+def test_chain_in_a_graph_and_on_another_stream():
+    w, m, x, do, off, pair, k, E = training_case()
+    want = feed_forward(w, x, do, off, pair, k)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        again = feed_forward(w, x, do, off, pair, k)
+    stream.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
+    graph = torch.cuda.CUDAGraph()
+    xs, dos = x.clone(), do.clone()
+    with torch.cuda.graph(graph):
+        out = feed_forward(w, xs, dos, off, pair, k)
+    for i in range(3):
+        xs.copy_(x * (i + 1))
+        dos.copy_(do * 0.5 ** i)
+        graph.replay()
+        eager = feed_forward(w, xs, dos, off, pair, k)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, eager)), i
+
+
+def test_decode_step_beside_the_fp4_layer():
+    """A token's row through the experts and the combine, as the FP4 layer's stages are chained."""
+    g = gen(9)
+    T, k, E, H, I = 4, 2, 6, 256, 256
+    x = normal(g, T, H).to(BF)
+    ids, gates = moe.route_topk(normal(g, T, E), k)
+    _, off, pair, pos = moe.sort_permute(ids, E)
+    m = {n: make_weights(g, E, *s) for n, s in (("w1", (I, H)), ("w3", (I, H)), ("w2", (H, I)))}
+    xq, xs = moe.quant_fp8_block(x)
+    hq, hs, _, _ = moe.fp8_block_glu(moe.fp8_block_prepack_glu(*m["w1"], *m["w3"]), xq, xs, off, rows=pair, row_div=k)
+    o = moe.fp8_block_grouped(moe.fp8_block_prepack(*m["w2"]), hq, hs, off)
+    y = moe.combine(o, gates, pos, T, k, H)
+    xv = ref.rows(xq, xs)
+    want = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            _, _, (h, _) = ref.glu(xv[t:t + 1], ref.weights(m["w1"][0][e], m["w1"][1][e]),
+                                   ref.weights(m["w3"][0][e], m["w3"][1][e]))
+            want[t] += float(gates[t, j]) * (ref.weights(m["w2"][0][e], m["w2"][1][e]) @ h[0])
+    # h is off by half an e4m3 step (2^-4) at most, o by half a bf16 step
+    assert (y.double() - want).norm() < (2.0 ** -4 + 2.0 ** -8) * want.norm()
