@@ -27,8 +27,6 @@ constexpr int kStepRows = 32;
 constexpr int kPanel = kTile * kStepRows * 2;  // bytes of one operand's step
 constexpr int kBuf = 3 * kPanel;               // dy for each block of k, x
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-
 struct GradLaunch {
   Fp8bGradArgs a;
   int ntn, ntk;     // tiles of an expert

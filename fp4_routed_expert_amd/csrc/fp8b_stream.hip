@@ -1,7 +1,8 @@
 // FP8 products with block scales of 128 for few rows: y[s, n] = sum over blocks
 // b of sx[b, r] sw[n / 128, b] (sum_{k in b} xq[r, k] wq[e, n, k]).  One MFMA
-// (K = 128) is one block's sum; the two scales meet it in one fp32 multiply-add
-// per element, since they are no powers of two.
+// (K = 128) is one block's sum (four with exact products where the result stays in
+// fp32); the two scales meet it in one fp32 multiply-add per element, since they
+// are no powers of two.
 //
 // Weight streaming, bound by HBM: a workgroup owns two neighbouring weight
 // tiles (32 columns, or 16 columns of gate and up) of one expert, or one tile
@@ -48,14 +49,26 @@ __device__ __forceinline__ void load_step(Step<NT, TT>& p, const Source<NT, TT>&
   }
 }
 
-template <int NT, int TT>
+template <int NT, int TT, bool kExact>
 __device__ __forceinline__ void multiply(const Step<NT, TT>& p, v4f (&acc)[NT][TT]) {
   v4f d[NT][TT];
+  if constexpr (kExact) {
+    Wide x[TT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int i = 0; i < TT; ++i) x[i] = widen(cat_pieces(p.x[i][0], p.x[i][1]));
 #pragma unroll
-    for (int i = 0; i < TT; ++i)
-      d[t][i] = mfma_block(cat_pieces(p.w[t][0], p.w[t][1]), cat_pieces(p.x[i][0], p.x[i][1]));
+    for (int t = 0; t < NT; ++t) {
+      const Wide w = widen(cat_pieces(p.w[t][0], p.w[t][1]));
+#pragma unroll
+      for (int i = 0; i < TT; ++i) d[t][i] = mfma_wide(w, x[i]);
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
+        d[t][i] = mfma_block(cat_pieces(p.w[t][0], p.w[t][1]), cat_pieces(p.x[i][0], p.x[i][1]));
+  }
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -70,7 +83,7 @@ __device__ __forceinline__ void multiply(const Step<NT, TT>& p, v4f (&acc)[NT][T
 // and up where they are wanted.
 template <int NW, int NT, int TT, int kB, Fp8bOut kOut>
 __global__ __launch_bounds__(64 * NW) void stream_kernel(Fp8bArgs a, Fp8bLayout L) {
-  constexpr bool kGlu = kOut == Fp8bOut::kGlu;
+  constexpr bool kGlu = kOut == Fp8bOut::kGlu, kExact = kOut == Fp8bOut::kFp32;
   static_assert(NT == 2 || (NT == 1 && !kGlu), "a gate tile with its up tile");
   constexpr int kRows = 16 * TT;
   __shared__ v4f red[NW][NT * TT][64];
@@ -123,11 +136,11 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(Fp8bArgs a, Fp8bLayout 
 #pragma unroll
       for (int b = 0; b < kB; ++b) load_step(p[b], src, wave + NW * (u + b));
 #pragma unroll
-      for (int b = 0; b < kB; ++b) multiply(p[b], acc);
+      for (int b = 0; b < kB; ++b) multiply<NT, TT, kExact>(p[b], acc);
     }
     for (; u < nsteps; ++u) {
       load_step(p[0], src, wave + NW * u);
-      multiply(p[0], acc);
+      multiply<NT, TT, kExact>(p[0], acc);
     }
     const int nb = (rows + 15) / 16;
 #pragma unroll

@@ -46,7 +46,11 @@ constexpr int kTop = kState + kWaves * 64;     // largest magnitudes that the wa
 constexpr int kLds = kTop + kWaves * 256;
 static_assert(kStage % 1024 == 0 && kLds <= 160 * 1024, "LDS");
 
-// Rows of an item.  A group's tiles of at most 256 rows are of equal heights.
+// With exact products (results that stay in fp32) a wave takes at most two token
+// tiles, whose bf16 values it keeps: 128 rows an item.
+constexpr int kWideSubs = 2;
+
+// Rows of an item.  A group's tiles are of equal heights.
 struct Tile {
   int row0, n;
 };
@@ -67,8 +71,8 @@ __host__ __device__ __forceinline__ float item_units(uint32_t tiles, int ntn, fl
 long tile_cap(long P, int E) { return P / 64 + (P < E ? P : E); }
 size_t rows_at(long P, int E) { return PackedLayout::align256(16 + 16 * (size_t)tile_cap(P, E)); }
 
-// Block 0 lists the tiles, the others look the rows up.
-__global__ __launch_bounds__(1024) void tiles_kernel(Fp8bArgs a, int E, int ntn, float per_cu, int cap,
+// Block 0 lists the tiles (of at most 64 `most` rows), the others look the rows up.
+__global__ __launch_bounds__(1024) void tiles_kernel(Fp8bArgs a, int E, int ntn, float per_cu, int most, int cap,
                                                      int32_t* __restrict__ ws, int32_t* __restrict__ xrows) {
   const int P = a.P;
   if (blockIdx.x > 0) {
@@ -103,8 +107,9 @@ __global__ __launch_bounds__(1024) void tiles_kernel(Fp8bArgs a, int E, int ntn,
   float best = 0.0f;
 #pragma unroll
   for (int i = 3; i >= 0; --i) {
+    if (i >= most) continue;
     const float units = item_units(all[i], ntn, per_cu, i + 1);
-    if (i == 3 || units < best)
+    if (i == most - 1 || units < best)
       best = units, nt = count[i], at = __builtin_elementwise_add_sat(before[i], incl[i] - nt), total = all[i];
   }
   if (e == 0) ws[0] = min(total, (uint32_t)cap);
@@ -318,7 +323,7 @@ __device__ __forceinline__ float lds_f32(uint32_t addr) { return __int_as_float(
 // weight tile and its token tiles, ad.w and the scales' addresses are in it, and
 // ad.x0 and ad.x1 in the other one, whose place is free: the cursor's stage goes
 // there.  On exit the same for the next stage.
-template <int S, bool kGlu>
+template <int S, bool kGlu, bool kWide>
 __device__ __forceinline__ void step(Ctx& c, Cursor& k, Addr& ad, int& stage, v4f (&acc)[8][4], Regs<S>& f) {
   c.l16 = opaque(c.l16);
   const uint32_t nxt = wave_u32(c.lds + (uint32_t)((stage ^ 1) * kStage));
@@ -333,6 +338,41 @@ __device__ __forceinline__ void step(Ctx& c, Cursor& k, Addr& ad, int& stage, v4
     for (int u = 0; u < kLoads; ++u) issue(c, k, nxt, u);
     advance(c, k);
     publish();
+  } else if constexpr (kWide) {
+    float ks[S];
+    Wide x[S];
+#pragma unroll
+    for (int t = 0; t < S; ++t) {
+      ks[t] = lds_f32((t & 1 ? ad.s1 : ad.s0) + 256 * (t >> 1)) * lds_f32(ad.sw);
+      x[t] = widen(f.b[t]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const Wide w = widen(f.a[i & 1]);
+      if (i == 7) {
+        publish();
+        ad.w = opaque(ad.w + flip);
+#pragma unroll
+        for (int t = 0; t < S; ++t) f.b[t] = read_x(ad, t);
+      }
+      f.a[(i + 1) & 1] = read_w(ad, (i + 1) & 7);
+#pragma unroll
+      for (int t = 0; t < S; ++t) {
+        const v4f d = mfma_wide(w, x[t]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(d[v], ks[t], acc[i][t][v]);
+        asm volatile("" : "+v"(acc[i][t]));
+      }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+        if (u / 2 == i) issue(c, k, nxt, u);
+    }
+    advance(c, k);
+    ad.x0 = opaque(ad.x0 - flip);
+    ad.x1 = opaque(ad.x1 - flip);
+    ad.sw = opaque(ad.sw + flip);
+    ad.s0 = opaque(ad.s0 + flip);
+    ad.s1 = opaque(ad.s1 + flip);
   } else {
     constexpr int kLag = 3;      // MFMAs between one and its multiply-adds
     constexpr int M = 8 * S;
@@ -561,7 +601,7 @@ __device__ __forceinline__ void run_item(Ctx& c, Cursor& k, int& stage, const Ti
     ad.x0 = opaque(ad.x0 + (other - cur));
     ad.x1 = opaque(ad.x1 + (other - cur));
   }
-  for (int j = 0; j < c.J; ++j) step<S, kGlu>(c, k, ad, stage, acc, f);
+  for (int j = 0; j < c.J; ++j) step<S, kGlu, kOut == Fp8bOut::kFp32>(c, k, ad, stage, acc, f);
   if constexpr (kOut == Fp8bOut::kGlu)
     store_glu<S>(c, acc, t, sub0, tn);
   else if constexpr (kOut == Fp8bOut::kGluGrad)
@@ -614,25 +654,30 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     const Tile t{(int)wave_u32(info.x), (int)wave_u32(info.y)};
     const int tn = (int)wave_u32(info.z);
     const int sub0 = first_sub(t.n, wm), live = sub_tiles(t.n, wm);
-    switch (live) {
-      case 0: run_item<0, kOut>(c, k, stage, t, sub0, tn); break;
-      case 1: run_item<1, kOut>(c, k, stage, t, sub0, tn); break;
-      case 2: run_item<2, kOut>(c, k, stage, t, sub0, tn); break;
-      case 3: run_item<3, kOut>(c, k, stage, t, sub0, tn); break;
-      default: run_item<4, kOut>(c, k, stage, t, sub0, tn); break;
+    if (live == 0) {
+      run_item<0, kOut>(c, k, stage, t, sub0, tn);
+    } else if (live == 1) {
+      run_item<1, kOut>(c, k, stage, t, sub0, tn);
+    } else if (kOut == Fp8bOut::kFp32 || live == 2) {
+      run_item<2, kOut>(c, k, stage, t, sub0, tn);
+    } else if constexpr (kOut != Fp8bOut::kFp32) {
+      if (live == 3)
+        run_item<3, kOut>(c, k, stage, t, sub0, tn);
+      else
+        run_item<4, kOut>(c, k, stage, t, sub0, tn);
     }
   }
   wait_vmcnt<0>();  // the dummy stages land before the LDS is given back
 }
 
 // Row tiles of a product of one group of P rows and ntn columns of items.
-int dense_tiles(int P, int ntn) {
+int dense_tiles(int P, int ntn, int most) {
   int tiles = 0;
   float best = 0.0f;
-  for (int s = 4; s > 0; --s) {
+  for (int s = most; s > 0; --s) {
     const int t = (P + 64 * s - 1) / (64 * s);
     const float units = item_units(t, ntn, 1.0f / (float)workgroups(), s);
-    if (s == 4 || units < best) best = units, tiles = t;
+    if (s == most || units < best) best = units, tiles = t;
   }
   return tiles;
 }
@@ -643,18 +688,19 @@ size_t fp8b_tiled_ws_bytes(long P, int E) { return rows_at(P, E) + 4 * (size_t)P
 
 hipError_t launch_fp8b_tiled(const Fp8bArgs& a, const Fp8bLayout& L, Fp8bOut out, void* ws, hipStream_t st) {
   const int ntn = (L.NT + kBT - 1) / kBT;
+  const int most = out == Fp8bOut::kFp32 ? kWideSubs : 4;
   Launch g{a, L, nullptr, nullptr, 0, 0};
   if (a.offsets) {
     int32_t* list = static_cast<int32_t*>(ws);
     int32_t* xrows = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + rows_at(a.P, L.E));
     hipLaunchKernelGGL(tiles_kernel, dim3(1 + (a.rows ? ((unsigned)a.P + 1023u) / 1024 : 0)), dim3(1024), 0, st, a, L.E,
-                       ntn, 1.0f / (float)workgroups(), (int)tile_cap(a.P, L.E), list, xrows);
+                       ntn, 1.0f / (float)workgroups(), most, (int)tile_cap(a.P, L.E), list, xrows);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     g.ws = list;
     g.xrows = a.rows ? xrows : nullptr;
   } else {
-    g.tiles = dense_tiles(a.P, ntn);
+    g.tiles = dense_tiles(a.P, ntn, most);
     g.height = tile_height(a.P, g.tiles);
   }
   const dim3 grid((unsigned)workgroups()), block(64 * kWaves);
