@@ -15,13 +15,19 @@
 // where their wait states are covered.  The accumulators have to lie in vector
 // registers, 128 of them.
 //
-// Stages are one block of K: 32 KiB of row pieces (128 bytes of each row), 32 KiB
-// of weight tiles and the scales, from global memory to LDS by LDS-DMA into two
-// stages.  One barrier per stage, in front of its last weight tile, publishes the
-// next stage and frees this one, which is refilled behind the first MFMAs of the
-// next.  Every wave issues the same nine loads per stage, dummy stages past
-// the end.  Row r's eight 16-byte pieces lie at piece p ^ (r / 2 % 8), which
-// spreads the 16 rows that one LDS cycle serves over all banks.
+// Stages are one block of K: 32 KiB of row pieces (128 bytes of each row), two
+// halves of 16 KiB of weight tiles and the scales, from global memory to LDS by
+// LDS-DMA.  A wave's token tiles go to registers before the stage begins, so the
+// row pieces are free in its middle: two places of them and five of weight halves
+// keep the loads of a stage two stages ahead (with two places of everything the
+// loads had one stage, and a stage took 1.2 us however few its rows: K 16384, N
+// 7168, 4604 rows 442 us).  Two barriers a stage: in its middle, which
+// publishes the second weight half and frees the row pieces and the first half,
+// and in front of its last weight tile, which publishes the next stage's rows and
+// first half and frees the second.  Every wave issues the same nine loads per stage
+// in the same order, dummy stages past the end, so that one wait count serves every
+// barrier.  Row r's eight 16-byte pieces lie at piece p ^ (r / 2 % 8), which spreads
+// the 16 rows that one LDS cycle serves over all banks.
 //
 // The workgroups are persistent: one per CU (its LDS allows no second) walks its
 // XCD's contiguous share of the items, and the stages run on across items.
@@ -35,16 +41,17 @@ constexpr int kBM = 256;              // rows of an item
 constexpr int kBT = 16;               // weight tiles of an item
 constexpr int kWaves = 8;
 constexpr int kX = kBM * 128;         // row pieces of a stage
-constexpr int kW = kBT * 2048;        // weight tiles
 constexpr int kS = kWaves * 256;      // scales: each wave's 32 rows and the item's two row blocks
-constexpr int kOffW = kX, kOffS = kX + kW;
-constexpr int kStage = kX + kW + kS;
-constexpr int kIdx = 2 * kStage;               // the next item's row indices
+constexpr int kHalf = kBT / 2 * 2048; // half the weight tiles: the first or the last four of either wave column
+constexpr int kHalves = 5;
+constexpr int kOffS = 2 * kX;                  // behind two places of row pieces two of scales
+constexpr int kOffW = kOffS + 2 * kS;          // and five of weight halves
+constexpr int kIdx = kOffW + kHalves * kHalf;  // the next item's row indices
 constexpr int kInfo = kIdx + kWaves * 256;     // for each wave eight items' (first row, rows, column)
 constexpr int kState = kInfo + kWaves * 128;   // and where its cursor goes next
 constexpr int kTop = kState + kWaves * 64;     // largest magnitudes that the waves of a row exchange
 constexpr int kLds = kTop + kWaves * 256;
-static_assert(kStage % 1024 == 0 && kLds <= 160 * 1024, "LDS");
+static_assert(kLds <= 160 * 1024, "LDS");
 
 // With exact products (results that stay in fp32) a wave takes at most two token
 // tiles, whose bf16 values it keeps: 128 rows an item.
@@ -163,7 +170,8 @@ __device__ __forceinline__ void next_item(const claunch* g, Walk& k) {
 // Where the DMA stands: the next stage to load of the item it is in.
 struct Cursor {
   const uint8_t* x;   // activation codes (uniform)
-  const uint8_t* w;   // the wave's two weight tiles (uniform)
+  const uint8_t* w;   // the wave's weight tile of the first half (uniform)
+  uint32_t w1;        // bytes from it to the second half's
   const uint8_t* s;   // per lane: its scale (lanes 0-31 of rows 32 w + l, the others of a weight block)
   uint32_t a[4];      // per lane: its piece of rows 32 w + 8 u + l / 8
   int left;           // stages left of the item (this one counted)
@@ -245,28 +253,30 @@ __device__ __forceinline__ void enter(const Ctx& c, Cursor& k, Walk& walk) {
   const float* ws = reinterpret_cast<const float*>(g->a.packed + g->L.s_off) + ((size_t)walk.e * g->L.NB + block) * J;
   k.s = reinterpret_cast<const uint8_t*>(c.lane() < 32 ? g->a.xs + row(c.lane() & 31) : ws);
   k.x = wave_ptr(g->a.xq);
-  // tiles past the last ones read those; their columns are not stored
-  const int nt = min(tn * kBT + 2 * c.wave, g->L.NT - 2);
+  // tiles past the last one read that; their columns are not stored
+  const int nt = min(tn * kBT + c.wave + 4 * (c.wave >> 2), g->L.NT - 1), nt1 = min(nt + 4, g->L.NT - 1);
   k.w = wave_ptr(g->a.packed + ((size_t)walk.e * g->L.NT + nt) * ((size_t)J * 2048));
+  k.w1 = wave_u32((uint32_t)(nt1 - nt) * (uint32_t)J * 2048u);
   k.left = c.J;
   next_item(g, walk);
 }
 
-// Load u (< 9) of the wave's share of the cursor's stage into the one at S: 0-3
-// row pieces, 4 scales, 5-8 weights.
+// Load u (< 9) of the wave's share of the cursor's stage: 0-1 the first weight
+// half into place W0, 2-5 row pieces and 6 scales into place p (0, 1), 7-8 the
+// second weight half into place W1.
 constexpr int kLoads = 9;
-__device__ __forceinline__ void issue(const Ctx& c, const Cursor& k, uint32_t S, int u) {
-  const uint32_t w = (uint32_t)c.wave, l16 = c.l16;
+__device__ __forceinline__ void issue(const Ctx& c, const Cursor& k, int p, uint32_t W0, uint32_t W1, int u) {
+  const uint32_t w = (uint32_t)c.wave, l16 = c.l16, X = c.lds + (uint32_t)(p * kX) + 4096u * w;
   switch (u) {
-    case 0: dma16(k.x, k.a[0], S + 4096u * w); break;
-    case 1: dma16(k.x, k.a[1], S + 4096u * w + 1024u); break;
-    case 2: dma16(k.x, k.a[2], S + 4096u * w + 2048u); break;
-    case 3: dma16(k.x, k.a[3], S + 4096u * w + 3u * 1024u); break;
-    case 4: dma4_lanes(k.s, S + (uint32_t)kOffS + 256u * w); break;
-    case 5: dma16(k.w, l16, S + (uint32_t)kOffW + 4096u * w); break;
-    case 6: dma16<1024>(k.w, l16, S + (uint32_t)kOffW + 4096u * w); break;
-    case 7: dma16(k.w + (size_t)c.J * 2048, l16, S + (uint32_t)kOffW + 4096u * w + 2048u); break;
-    default: dma16<1024>(k.w + (size_t)c.J * 2048, l16, S + (uint32_t)kOffW + 4096u * w + 2048u);
+    case 0: dma16(k.w, l16, W0 + 2048u * w); break;
+    case 1: dma16<1024>(k.w, l16, W0 + 2048u * w); break;
+    case 2: dma16(k.x, k.a[0], X); break;
+    case 3: dma16(k.x, k.a[1], X + 1024u); break;
+    case 4: dma16(k.x, k.a[2], X + 2048u); break;
+    case 5: dma16(k.x, k.a[3], X + 3u * 1024u); break;
+    case 6: dma4_lanes(k.s, c.lds + (uint32_t)(kOffS + p * kS) + 256u * w); break;
+    case 7: dma16(k.w + k.w1, l16, W1 + 2048u * w); break;
+    default: dma16<1024>(k.w + k.w1, l16, W1 + 2048u * w);
   }
 }
 
@@ -284,10 +294,10 @@ __device__ __forceinline__ void advance(const Ctx& c, Cursor& k) {
   }
   Walk walk = load_walk(c);
   if (!walk.more) return;
-  // the indices were loaded a stage after the cursor entered this item, and the
-  // wait in front of a barrier has covered them since
-  if (c.J == 1) {
-    fetch_rows(c, walk);
+  // the indices were loaded a stage after the cursor entered this item; two stages
+  // of loads behind them, the waits have covered them
+  if (c.J < 3) {
+    if (c.J == 1) fetch_rows(c, walk);
     wait_vmcnt<0>();
   }
   enter(c, k, walk);
@@ -295,13 +305,22 @@ __device__ __forceinline__ void advance(const Ctx& c, Cursor& k) {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the indices are read before they are replaced
 }
 
-// LDS addresses of a lane, flipped between the two stages as the loop goes on.
+// LDS addresses of a lane, moved from place to place as the loop goes on.
 struct Addr {
   uint32_t x0, x1;  // the two pieces of row r of the wave's first token tile (tile i at + 2048 i)
-  uint32_t w;       // weight tile 8 wn (tile i at + 2048 i, its second half at + 1024)
+  uint32_t w;       // the wave's first weight tile of a half (tile i at + 2048 i, its second half at + 1024)
   uint32_t sw;      // the first of the wave's weight scales
   uint32_t s0, s1;  // the row's scale in the first and the second token tile (two tiles on: + 256)
 };
+
+// Where the loop stands: the stage's parity, and the places of its first weight
+// half and of the one that is loaded next.
+struct Place {
+  int p;
+  int read, load;
+};
+__device__ __forceinline__ int next_half(int h) { return h == kHalves - 1 ? 0 : h + 1; }
+__device__ __forceinline__ uint32_t half_at(const Ctx& c, int h) { return wave_u32(c.lds + (uint32_t)(kOffW + h * kHalf)); }
 
 template <int S>
 struct Regs {
@@ -311,6 +330,7 @@ struct Regs {
 template <>
 struct Regs<0> {};
 
+// weight tile i of a half
 __device__ __forceinline__ v8i read_w(const Addr& ad, int i) {
   return cat_pieces(lds_v4(ad.w + 2048 * i), lds_v4(ad.w + 2048 * i + 1024));
 }
@@ -319,64 +339,35 @@ __device__ __forceinline__ v8i read_x(const Addr& ad, int i) {
 }
 __device__ __forceinline__ float lds_f32(uint32_t addr) { return __int_as_float(lds_i32(addr)); }
 
+// A barrier of the loop: the loads that it publishes have landed (behind them this
+// wave has issued eleven more), and this wave's LDS reads are done; then everyone's.
+__device__ __forceinline__ void publish() {
+  static_assert(kLoads + 2 == 11, "a stage and a weight half");
+  asm volatile("s_waitcnt vmcnt(11) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // One stage for a wave with S live token tiles.  On entry f holds its first
-// weight tile and its token tiles, ad.w and the scales' addresses are in it, and
-// ad.x0 and ad.x1 in the other one, whose place is free: the cursor's stage goes
-// there.  On exit the same for the next stage.
+// weight tile and its token tiles, ad.w is in its first weight half, the scales'
+// addresses in its scales, ad.x0 and ad.x1 in the next stage's rows.  On exit the
+// same for the next stage.
 template <int S, bool kGlu, bool kWide>
-__device__ __forceinline__ void step(Ctx& c, Cursor& k, Addr& ad, int& stage, v4f (&acc)[8][4], Regs<S>& f) {
+__device__ __forceinline__ void step(Ctx& c, Cursor& k, Addr& ad, Place& at, v4f (&acc)[8][4], Regs<S>& f) {
   c.l16 = opaque(c.l16);
-  const uint32_t nxt = wave_u32(c.lds + (uint32_t)((stage ^ 1) * kStage));
-  const uint32_t flip = wave_u32((uint32_t)(stage ? -kStage : kStage));
-  auto publish = [] {
-    // This wave's loads of the next stage have landed and its reads of this one
-    // are done; then everyone's.
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  };
+  const int load1 = next_half(at.load), read1 = next_half(at.read), read2 = next_half(read1);
+  const uint32_t W0 = half_at(c, at.load), W1 = half_at(c, load1);
+  auto load = [&](int u) { issue(c, k, at.p, W0, W1, u); };
   if constexpr (S == 0) {
+    load(0);
+    load(1);
+    publish();
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) issue(c, k, nxt, u);
+    for (int u = 2; u < kLoads; ++u) load(u);
     advance(c, k);
     publish();
-  } else if constexpr (kWide) {
-    float ks[S];
-    Wide x[S];
-#pragma unroll
-    for (int t = 0; t < S; ++t) {
-      ks[t] = lds_f32((t & 1 ? ad.s1 : ad.s0) + 256 * (t >> 1)) * lds_f32(ad.sw);
-      x[t] = widen(f.b[t]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const Wide w = widen(f.a[i & 1]);
-      if (i == 7) {
-        publish();
-        ad.w = opaque(ad.w + flip);
-#pragma unroll
-        for (int t = 0; t < S; ++t) f.b[t] = read_x(ad, t);
-      }
-      f.a[(i + 1) & 1] = read_w(ad, (i + 1) & 7);
-#pragma unroll
-      for (int t = 0; t < S; ++t) {
-        const v4f d = mfma_wide(w, x[t]);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(d[v], ks[t], acc[i][t][v]);
-        asm volatile("" : "+v"(acc[i][t]));
-      }
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u)
-        if (u / 2 == i) issue(c, k, nxt, u);
-    }
-    advance(c, k);
-    ad.x0 = opaque(ad.x0 - flip);
-    ad.x1 = opaque(ad.x1 - flip);
-    ad.sw = opaque(ad.sw + flip);
-    ad.s0 = opaque(ad.s0 + flip);
-    ad.s1 = opaque(ad.s1 + flip);
   } else {
-    constexpr int kLag = 3;      // MFMAs between one and its multiply-adds
-    constexpr int M = 8 * S;
-    constexpr int kSpread = S == 1 ? 5 : kLoads;  // the loads stand behind the first MFMAs
+    // addresses on from a place to the next one
+    const uint32_t hop1 = wave_u32((uint32_t)((read1 - at.read) * kHalf)), hop2 = wave_u32((uint32_t)((read2 - read1) * kHalf));
+    const uint32_t flip = wave_u32((uint32_t)(at.p ? -1 : 1));
     float ks[S], ku[S];
     {
       const float w0 = lds_f32(ad.sw), w1 = kGlu ? lds_f32(ad.sw + 4) : 0.0f;
@@ -387,40 +378,79 @@ __device__ __forceinline__ void step(Ctx& c, Cursor& k, Addr& ad, int& stage, v4
         if constexpr (kGlu) ku[t] = sx * w1;
       }
     }
-    v4f d[kLag + 1];
-    auto add = [&](int m) {
-      const int i = m / S, t = m % S;
-      const float s = kGlu && (i & 1) ? ku[t] : ks[t];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(d[m & kLag][v], s, acc[i][t][v]);
-      asm volatile("" : "+v"(acc[i][t]));  // here, not behind the branches of advance()
-    };
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const int i = m / S, t = m % S;
-      d[m & kLag] = mfma_block(f.a[i & 1], f.b[t]);
-      if (m >= kLag) add(m - kLag);
-      if (m == 7 * S) {
+    // In front of the reads of row i's successor: the barriers, and the weight halves' ends.
+    auto turn = [&](int i) {
+      if (i == 3 || i == 7) {
         publish();
-        ad.w = opaque(ad.w + flip);
+        ad.w = opaque(ad.w + (i == 3 ? hop1 : hop2));
       }
-      if (t == 0) f.a[(i + 1) & 1] = read_w(ad, (i + 1) & 7);
-      if (i == 7) f.b[t] = read_x(ad, t);
+    };
+    if constexpr (kWide) {
+      Wide x[S];
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u)
-        if (u * kSpread / kLoads == m) issue(c, k, nxt, u);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int t = 0; t < S; ++t) x[t] = widen(f.b[t]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const Wide w = widen(f.a[i & 1]);
+        turn(i);
+        f.a[(i + 1) & 1] = read_w(ad, (i + 1) & 3);
+        if (i == 7) {
+#pragma unroll
+          for (int t = 0; t < S; ++t) f.b[t] = read_x(ad, t);
+        }
+#pragma unroll
+        for (int t = 0; t < S; ++t) {
+          const v4f d = mfma_wide(w, x[t]);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(d[v], ks[t], acc[i][t][v]);
+          asm volatile("" : "+v"(acc[i][t]));
+        }
+        if (i == 0) load(0), load(1);
+        if (i >= 3 && i < 7) load(2 * i - 4);
+        if (i >= 3 && i < 6) load(2 * i - 3);
+      }
+    } else {
+      constexpr int kLag = 3;  // MFMAs between one and its multiply-adds
+      constexpr int M = 8 * S;
+      v4f d[kLag + 1];
+      auto add = [&](int m) {
+        const int i = m / S, t = m % S;
+        const float s = kGlu && (i & 1) ? ku[t] : ks[t];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(d[m & kLag][v], s, acc[i][t][v]);
+        asm volatile("" : "+v"(acc[i][t]));  // here, not behind the branches of advance()
+      };
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const int i = m / S, t = m % S;
+        d[m & kLag] = mfma_block(f.a[i & 1], f.b[t]);
+        if (m >= kLag) add(m - kLag);
+        if (t == 0) {
+          turn(i);
+          f.a[(i + 1) & 1] = read_w(ad, (i + 1) & 3);
+        }
+        if (i == 7) f.b[t] = read_x(ad, t);
+        // the loads of two stages on: the first weight half at once, the rest behind the middle
+        if (m == 0) load(0);
+        if (m == (S > 1 ? 1 : 0)) load(1);
+#pragma unroll
+        for (int u = 2; u < kLoads; ++u)
+          if (3 * S + (u - 2) * (S < 3 ? 4 * S : 8) / 7 == m) load(u);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int m = (M > kLag ? M - kLag : 0); m < M; ++m) add(m);
     }
-#pragma unroll
-    for (int m = (M > kLag ? M - kLag : 0); m < M; ++m) add(m);
     advance(c, k);  // here, where the fewest registers are taken
-    ad.x0 = opaque(ad.x0 - flip);
-    ad.x1 = opaque(ad.x1 - flip);
-    ad.sw = opaque(ad.sw + flip);
-    ad.s0 = opaque(ad.s0 + flip);
-    ad.s1 = opaque(ad.s1 + flip);
+    ad.x0 = opaque(ad.x0 - flip * kX);
+    ad.x1 = opaque(ad.x1 - flip * kX);
+    ad.sw = opaque(ad.sw + flip * kS);
+    ad.s0 = opaque(ad.s0 + flip * kS);
+    ad.s1 = opaque(ad.s1 + flip * kS);
   }
-  stage ^= 1;
+  at.p ^= 1;
+  at.read = read2;
+  at.load = next_half(load1);
 }
 
 __device__ __forceinline__ void nt_store16(void* p, v4u v) {
@@ -577,20 +607,20 @@ __device__ __forceinline__ void store_grad(const Ctx& c, v4f (&acc)[8][4], const
 }
 
 template <int S, Fp8bOut kOut>
-__device__ __forceinline__ void run_item(Ctx& c, Cursor& k, int& stage, const Tile& t, int sub0, int tn) {
+__device__ __forceinline__ void run_item(Ctx& c, Cursor& k, Place& at, const Tile& t, int sub0, int tn) {
   constexpr bool kGlu = kOut == Fp8bOut::kGlu;
   v4f acc[8][4];
   Regs<S> f;
   Addr ad;
   if constexpr (S > 0) {
     const int r = c.lane() & 15, g = c.lane() >> 4, wn = c.wave & 1;
-    const uint32_t cur = c.lds + (uint32_t)(stage * kStage), other = c.lds + (uint32_t)((stage ^ 1) * kStage);
-    ad.x0 = opaque(cur + (uint32_t)(16 * sub0 + r) * 128 + (((uint32_t)(g ^ (r >> 1)) & 7) << 4));
-    ad.x1 = opaque(cur + (uint32_t)(16 * sub0 + r) * 128 + (((uint32_t)(g ^ (r >> 1) ^ 4) & 7) << 4));
-    ad.w = opaque(cur + (uint32_t)(kOffW + 16384 * wn + c.l16));
-    ad.sw = opaque(cur + (uint32_t)(kOffS + 256 * c.wave + 128 + (kGlu ? 0 : 4 * wn)));
-    ad.s0 = opaque(cur + (uint32_t)(kOffS + 256 * (sub0 >> 1) + 64 * (sub0 & 1) + 4 * r));
-    ad.s1 = opaque(cur + (uint32_t)(kOffS + 256 * ((sub0 + 1) >> 1) + 64 * ((sub0 + 1) & 1) + 4 * r));
+    const uint32_t X = c.lds + (uint32_t)(at.p * kX), sc = c.lds + (uint32_t)(kOffS + at.p * kS);
+    ad.x0 = opaque(X + (uint32_t)(16 * sub0 + r) * 128 + (((uint32_t)(g ^ (r >> 1)) & 7) << 4));
+    ad.x1 = opaque(X + (uint32_t)(16 * sub0 + r) * 128 + (((uint32_t)(g ^ (r >> 1) ^ 4) & 7) << 4));
+    ad.w = opaque(half_at(c, at.read) + (uint32_t)(8192 * wn) + c.l16);
+    ad.sw = opaque(sc + (uint32_t)(256 * c.wave + 128 + (kGlu ? 0 : 4 * wn)));
+    ad.s0 = opaque(sc + (uint32_t)(256 * (sub0 >> 1) + 64 * (sub0 & 1) + 4 * r));
+    ad.s1 = opaque(sc + (uint32_t)(256 * ((sub0 + 1) >> 1) + 64 * ((sub0 + 1) & 1) + 4 * r));
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -598,10 +628,11 @@ __device__ __forceinline__ void run_item(Ctx& c, Cursor& k, int& stage, const Ti
     f.a[0] = read_w(ad, 0);
 #pragma unroll
     for (int q = 0; q < S; ++q) f.b[q] = read_x(ad, q);
-    ad.x0 = opaque(ad.x0 + (other - cur));
-    ad.x1 = opaque(ad.x1 + (other - cur));
+    const uint32_t flip = (uint32_t)(at.p ? -kX : kX);
+    ad.x0 = opaque(ad.x0 + flip);
+    ad.x1 = opaque(ad.x1 + flip);
   }
-  for (int j = 0; j < c.J; ++j) step<S, kGlu, kOut == Fp8bOut::kFp32>(c, k, ad, stage, acc, f);
+  for (int j = 0; j < c.J; ++j) step<S, kGlu, kOut == Fp8bOut::kFp32>(c, k, ad, at, acc, f);
   if constexpr (kOut == Fp8bOut::kGlu)
     store_glu<S>(c, acc, t, sub0, tn);
   else if constexpr (kOut == Fp8bOut::kGluGrad)
@@ -642,12 +673,15 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     store_walk(c, walk);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
-  const uint32_t s0 = wave_u32(c.lds);
+  // two stages ahead, into the places 0, 1 and 2, 3 of the weight halves
 #pragma unroll
-  for (int u = 0; u < kLoads; ++u) issue(c, k, s0, u);
-  advance(c, k);
-  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-  int stage = 0;
+  for (int p = 0; p < 2; ++p) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) issue(c, k, p, half_at(c, 2 * p), half_at(c, 2 * p + 1), u);
+    advance(c, k);
+  }
+  publish();
+  Place at{0, 0, 4};
   for (int i = 0; i < mine; ++i) {
     // as the cursor noted it
     const v4u info = lds_v4(c.lds + kInfo + 128 * wave + 16 * (i & 7));
@@ -655,16 +689,16 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     const int tn = (int)wave_u32(info.z);
     const int sub0 = first_sub(t.n, wm), live = sub_tiles(t.n, wm);
     if (live == 0) {
-      run_item<0, kOut>(c, k, stage, t, sub0, tn);
+      run_item<0, kOut>(c, k, at, t, sub0, tn);
     } else if (live == 1) {
-      run_item<1, kOut>(c, k, stage, t, sub0, tn);
+      run_item<1, kOut>(c, k, at, t, sub0, tn);
     } else if (kOut == Fp8bOut::kFp32 || live == 2) {
-      run_item<2, kOut>(c, k, stage, t, sub0, tn);
+      run_item<2, kOut>(c, k, at, t, sub0, tn);
     } else if constexpr (kOut != Fp8bOut::kFp32) {
       if (live == 3)
-        run_item<3, kOut>(c, k, stage, t, sub0, tn);
+        run_item<3, kOut>(c, k, at, t, sub0, tn);
       else
-        run_item<4, kOut>(c, k, stage, t, sub0, tn);
+        run_item<4, kOut>(c, k, at, t, sub0, tn);
     }
   }
   wait_vmcnt<0>();  // the dummy stages land before the LDS is given back
