@@ -21,10 +21,10 @@
 // row pieces are free in its middle: two places of them and five of weight halves
 // keep the loads of a stage two stages ahead (with two places of everything the
 // loads had one stage, and a stage took 1.2 us however few its rows: K 16384, N
-// 7168, 4604 rows 442 us).  Two barriers a stage: in its middle, which
-// publishes the second weight half and frees the row pieces and the first half,
-// and in front of its last weight tile, which publishes the next stage's rows and
-// first half and frees the second.  Every wave issues the same nine loads per stage
+// 7168, 256 rows 178 us, now 119).  Two barriers a stage: behind its first quarter,
+// which publishes the second weight half and frees the row pieces and the first
+// half, and behind its third, which publishes the next stage's rows and first half
+// and frees the second.  Every wave issues the same nine loads per stage
 // in the same order, dummy stages past the end, so that one wait count serves every
 // barrier.  Row r's eight 16-byte pieces lie at piece p ^ (r / 2 % 8), which spreads
 // the 16 rows that one LDS cycle serves over all banks.
@@ -318,13 +318,14 @@ struct Addr {
 struct Place {
   int p;
   int read, load;
+  int slack, stores;  // barriers that need not wait for the last item's stores, and how many those are, in fours
 };
 __device__ __forceinline__ int next_half(int h) { return h == kHalves - 1 ? 0 : h + 1; }
 __device__ __forceinline__ uint32_t half_at(const Ctx& c, int h) { return wave_u32(c.lds + (uint32_t)(kOffW + h * kHalf)); }
 
 template <int S>
 struct Regs {
-  v8i a[2];  // weight tiles
+  v8i a[4];  // weight tiles
   v8i b[S];  // token tiles of a stage
 };
 template <>
@@ -339,15 +340,45 @@ __device__ __forceinline__ v8i read_x(const Addr& ad, int i) {
 }
 __device__ __forceinline__ float lds_f32(uint32_t addr) { return __int_as_float(lds_i32(addr)); }
 
-// A barrier of the loop: the loads that it publishes have landed (behind them this
-// wave has issued eleven more), and this wave's LDS reads are done; then everyone's.
-__device__ __forceinline__ void publish() {
-  static_assert(kLoads + 2 == 11, "a stage and a weight half");
-  asm volatile("s_waitcnt vmcnt(11) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// A barrier of the loop: the loads that it publishes have landed (kBehind more have
+// been issued behind them), and this wave's LDS reads are done; then everyone's.
+// The first one of a stage publishes its second weight half, the last loads of two
+// stages before; the other one the next stage's rows, scales and first half, the
+// first seven loads of the stage before.  Behind an item's end stand its stores too
+// (vector memory operations complete in order): the loads that the next three
+// barriers publish are older, so that as many more may be outstanding and nothing
+// waits for the stores.
+constexpr int kFirst = kLoads + 2, kSecond = 2 + 7;
+template <int kBehind>
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kBehind) : "memory");
+}
+template <int kBehind>
+__device__ __forceinline__ void publish(Place& at) {
+  if (at.slack == 0) {
+    wait_and_meet<kBehind>();
+    return;
+  }
+  --at.slack;
+  switch (at.stores) {
+    case 1: wait_and_meet<kBehind + 4>(); break;
+    case 2: wait_and_meet<kBehind + 8>(); break;
+    case 3: wait_and_meet<kBehind + 12>(); break;
+    case 4: wait_and_meet<kBehind + 16>(); break;
+    case 5: wait_and_meet<kBehind + 20>(); break;
+    case 6: wait_and_meet<kBehind + 24>(); break;
+    case 7: wait_and_meet<kBehind + 28>(); break;
+    default: wait_and_meet<kBehind + 32>();
+  }
+}
+// After an item: at least n stores have been issued since its last loads.
+__device__ __forceinline__ void stored(Place& at, int n) {
+  at.stores = min(n / 4, 8);
+  at.slack = at.stores > 0 ? 3 : 0;
 }
 
-// One stage for a wave with S live token tiles.  On entry f holds its first
-// weight tile and its token tiles, ad.w is in its first weight half, the scales'
+// One stage for a wave with S live token tiles.  On entry f holds its first two
+// weight tiles and its token tiles, ad.w is in its first weight half, the scales'
 // addresses in its scales, ad.x0 and ad.x1 in the next stage's rows.  On exit the
 // same for the next stage.
 template <int S, bool kGlu, bool kWide>
@@ -357,44 +388,55 @@ __device__ __forceinline__ void step(Ctx& c, Cursor& k, Addr& ad, Place& at, v4f
   const uint32_t W0 = half_at(c, at.load), W1 = half_at(c, load1);
   auto load = [&](int u) { issue(c, k, at.p, W0, W1, u); };
   if constexpr (S == 0) {
-    load(0);
-    load(1);
-    publish();
 #pragma unroll
-    for (int u = 2; u < kLoads; ++u) load(u);
+    for (int u = 0; u < kLoads; ++u) {
+      if (u == 2) publish<kFirst>(at);
+      if (u == 7) publish<kSecond>(at);
+      load(u);
+    }
     advance(c, k);
-    publish();
   } else {
     // addresses on from a place to the next one
     const uint32_t hop1 = wave_u32((uint32_t)((read1 - at.read) * kHalf)), hop2 = wave_u32((uint32_t)((read2 - read1) * kHalf));
     const uint32_t flip = wave_u32((uint32_t)(at.p ? -1 : 1));
-    float ks[S], ku[S];
-    {
-      const float w0 = lds_f32(ad.sw), w1 = kGlu ? lds_f32(ad.sw + 4) : 0.0f;
+    float ks[S], ku[S], sx[S];
+    const float w0 = lds_f32(ad.sw), w1 = kGlu ? lds_f32(ad.sw + 4) : 0.0f;
+#pragma unroll
+    for (int t = 0; t < S; ++t) sx[t] = lds_f32((t & 1 ? ad.s1 : ad.s0) + 256 * (t >> 1));
+    auto scale_products = [&] {
 #pragma unroll
       for (int t = 0; t < S; ++t) {
-        const float sx = lds_f32((t & 1 ? ad.s1 : ad.s0) + 256 * (t >> 1));
-        ks[t] = sx * w0;
-        if constexpr (kGlu) ku[t] = sx * w1;
-      }
-    }
-    // In front of the reads of row i's successor: the barriers, and the weight halves' ends.
-    auto turn = [&](int i) {
-      if (i == 3 || i == 7) {
-        publish();
-        ad.w = opaque(ad.w + (i == 3 ? hop1 : hop2));
+        ks[t] = sx[t] * w0;
+        if constexpr (kGlu) ku[t] = sx[t] * w1;
       }
     };
+    // The weight tiles go in pairs, and a pair's MFMAs token tile by token tile, so
+    // that a token tile's registers are free for the next stage's six MFMAs before
+    // that needs them.  Behind the first MFMA of the second and the fourth pair stand
+    // the barriers: the tiles read from there on lie in another half.
+    auto turn = [&](int p) {
+      if (p == 1) publish<kFirst>(at);
+      if (p == 3) publish<kSecond>(at);
+      if (p == 1 || p == 3) {
+        ad.w = opaque(ad.w + (p == 1 ? hop1 : hop2));
+      }
+    };
+    // tile 2 p + 2 + h, read in pair p
+    auto ahead = [&](int p, int h) { f.a[(2 * p + 2 + h) & 3] = read_w(ad, (2 * p + 2 + h) & 3); };
     if constexpr (kWide) {
       Wide x[S];
 #pragma unroll
       for (int t = 0; t < S; ++t) x[t] = widen(f.b[t]);
+      scale_products();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const Wide w = widen(f.a[i & 1]);
-        turn(i);
-        f.a[(i + 1) & 1] = read_w(ad, (i + 1) & 3);
-        if (i == 7) {
+        const Wide w = widen(f.a[i & 3]);
+        if ((i & 1) == 0) {
+          turn(i >> 1);
+          ahead(i >> 1, 0);
+          ahead(i >> 1, 1);
+        }
+        if (i == 6) {
 #pragma unroll
           for (int t = 0; t < S; ++t) f.b[t] = read_x(ad, t);
         }
@@ -405,16 +447,18 @@ __device__ __forceinline__ void step(Ctx& c, Cursor& k, Addr& ad, Place& at, v4f
           for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(d[v], ks[t], acc[i][t][v]);
           asm volatile("" : "+v"(acc[i][t]));
         }
-        if (i == 0) load(0), load(1);
-        if (i >= 3 && i < 7) load(2 * i - 4);
-        if (i >= 3 && i < 6) load(2 * i - 3);
+        // (two in front of the first barrier, five in front of the second, two behind it)
+        if (i < 2) load(i);
+        if (i >= 2 && i < 6) load(i);
+        if (i == 5) load(6);
+        if (i >= 6) load(i + 1);
       }
     } else {
       constexpr int kLag = 3;  // MFMAs between one and its multiply-adds
       constexpr int M = 8 * S;
       v4f d[kLag + 1];
       auto add = [&](int m) {
-        const int i = m / S, t = m % S;
+        const int i = 2 * (m / (2 * S)) + (m & 1), t = m / 2 % S;
         const float s = kGlu && (i & 1) ? ku[t] : ks[t];
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(d[m & kLag][v], s, acc[i][t][v]);
@@ -422,20 +466,23 @@ __device__ __forceinline__ void step(Ctx& c, Cursor& k, Addr& ad, Place& at, v4f
       };
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        const int i = m / S, t = m % S;
-        d[m & kLag] = mfma_block(f.a[i & 1], f.b[t]);
+        const int p = m / (2 * S), at_p = m % (2 * S), h = m & 1, t = m / 2 % S;
+        d[m & kLag] = mfma_block(f.a[(2 * p + h) & 3], f.b[t]);
+        __builtin_amdgcn_sched_barrier(0);  // in front of a barrier, not behind it
+        if (m == kLag - 1) scale_products();  // their reads come back under the first MFMAs
         if (m >= kLag) add(m - kLag);
-        if (t == 0) {
-          turn(i);
-          f.a[(i + 1) & 1] = read_w(ad, (i + 1) & 3);
+        if (at_p == 0) {
+          turn(p);
+          ahead(p, 0);
         }
-        if (i == 7) f.b[t] = read_x(ad, t);
-        // the loads of two stages on: the first weight half at once, the rest behind the middle
-        if (m == 0) load(0);
-        if (m == (S > 1 ? 1 : 0)) load(1);
+        if (at_p == 1) ahead(p, 1);
+        if (p == 3 && h == 1) f.b[t] = read_x(ad, t);
+        // the loads of two stages on, spread over the stage: in front of the first
+        // barrier the first weight half, in front of the second rows and scales, behind
+        // it the second half
 #pragma unroll
-        for (int u = 2; u < kLoads; ++u)
-          if (3 * S + (u - 2) * (S < 3 ? 4 * S : 8) / 7 == m) load(u);
+        for (int u = 0; u < kLoads; ++u)
+          if ((u < 2 ? (2 * u + 1) * S / 2 : u < 7 ? 2 * S + (4 * u - 7) * S / 5 : 6 * S + (2 * u - 13) * S / 2) == m) load(u);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -464,7 +511,7 @@ __device__ __forceinline__ void nt_store8(void* p, uint32_t a, uint32_t b) {
 // token, a quad of lanes (g = 0..3) 32.  The stores are non-temporal: the outputs
 // would push rows and weights out of L2.
 template <int S, bool kF32>
-__device__ __forceinline__ void store_sums(const Ctx& c, const v4f (&acc)[8][4], const Tile& t, int sub0, int tn) {
+__device__ __forceinline__ int store_sums(const Ctx& c, const v4f (&acc)[8][4], const Tile& t, int sub0, int tn) {
   constexpr size_t kB = kF32 ? 4 : 2;
   const claunch* g = c.launch();
   const int N = g->L.N, r = c.lane() & 15, q = c.lane() >> 4, col0 = 256 * tn + 128 * (c.wave & 1);
@@ -489,12 +536,13 @@ __device__ __forceinline__ void store_sums(const Ctx& c, const v4f (&acc)[8][4],
     }
     __builtin_amdgcn_sched_barrier(0);
   }
+  return pairs > 0 ? S * pairs * (kF32 ? 2 : 1) : 0;
 }
 
 // SwiGLU, and the codes of its rows.  A wave has 64 columns of an item's 128; the
 // two waves of a row exchange their largest magnitudes through LDS.
 template <int S>
-__device__ __forceinline__ void store_glu(const Ctx& c, v4f (&acc)[8][4], const Tile& t, int sub0, int tn) {
+__device__ __forceinline__ int store_glu(const Ctx& c, v4f (&acc)[8][4], const Tile& t, int sub0, int tn) {
   const claunch* g = c.launch();
   const int N = g->L.N, r = c.lane() & 15, q = c.lane() >> 4;
   const size_t P = (size_t)g->a.P;
@@ -551,34 +599,39 @@ __device__ __forceinline__ void store_glu(const Ctx& c, v4f (&acc)[8][4], const 
       __builtin_amdgcn_sched_barrier(0);
     }
   }
+  return S * (g->a.gate ? 6 : 2);
 }
 
 // The sums are dh: dg and du of the wave's 128 columns, and their codes.
 template <int S>
-__device__ __forceinline__ void store_grad(const Ctx& c, v4f (&acc)[8][4], const Tile& t, int sub0, int tn) {
+__device__ __forceinline__ int store_grad(const Ctx& c, v4f (&acc)[8][4], const Tile& t, int sub0, int tn) {
   const claunch* g = c.launch();
   const int N = g->L.N, r = c.lane() & 15, q = c.lane() >> 4, nb = 2 * tn + (c.wave & 1), NB = N / 128;
-  if (nb >= NB) return;
+  if (nb >= NB) return 0;
   const size_t P = (size_t)g->a.P;
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    const int m = 16 * (sub0 + i) + r;
-    const size_t row = (size_t)(t.row0 + min(m, t.n - 1));
-    const uint16_t* gate = g->a.gate + row * N + 128 * nb + 8 * q;
-    const uint16_t* up = g->a.up + row * N + 128 * nb + 8 * q;
-    v4u eg[4], eu[4];
+  v4u eg[2][4], eu[2][4];
+  auto row_of = [&](int i) { return (size_t)(t.row0 + min(16 * (sub0 + i) + r, t.n - 1)); };
+  auto fetch = [&](int i) {
+    const size_t at = row_of(i) * N + 128 * nb + 8 * q;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      eg[p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(gate + 32 * p));
-      eu[p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(up + 32 * p));
+      eg[i & 1][p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(g->a.gate + at + 32 * p));
+      eu[i & 1][p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(g->a.up + at + 32 * p));
     }
+  };
+  if constexpr (S > 0) fetch(0);
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    if (i + 1 < S) fetch(i + 1);  // in front of this tile's stores, which its values would otherwise wait for
+    const int m = 16 * (sub0 + i) + r;
+    const size_t row = row_of(i);
     float du[32];
     uint32_t tg = 0, tu = 0;
 #pragma unroll
     for (int p = 0; p < 4; ++p)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t wg = eg[p][e >> 1], wu = eu[p][e >> 1];
+        const uint32_t wg = eg[i & 1][p][e >> 1], wu = eu[i & 1][p][e >> 1];
         const float gv = __uint_as_float(e & 1 ? wg & 0xFFFF0000u : wg << 16);
         const float uv = __uint_as_float(e & 1 ? wu & 0xFFFF0000u : wu << 16);
         float dg;
@@ -604,6 +657,7 @@ __device__ __forceinline__ void store_grad(const Ctx& c, v4f (&acc)[8][4], const
     }
     __builtin_amdgcn_sched_barrier(0);
   }
+  return 8 * S;
 }
 
 template <int S, Fp8bOut kOut>
@@ -626,6 +680,7 @@ __device__ __forceinline__ void run_item(Ctx& c, Cursor& k, Place& at, const Til
 #pragma unroll
       for (int q = 0; q < S; ++q) acc[i][q] = v4f{0.f, 0.f, 0.f, 0.f};
     f.a[0] = read_w(ad, 0);
+    f.a[1] = read_w(ad, 1);
 #pragma unroll
     for (int q = 0; q < S; ++q) f.b[q] = read_x(ad, q);
     const uint32_t flip = (uint32_t)(at.p ? -kX : kX);
@@ -633,12 +688,14 @@ __device__ __forceinline__ void run_item(Ctx& c, Cursor& k, Place& at, const Til
     ad.x1 = opaque(ad.x1 + flip);
   }
   for (int j = 0; j < c.J; ++j) step<S, kGlu, kOut == Fp8bOut::kFp32>(c, k, ad, at, acc, f);
+  int n;
   if constexpr (kOut == Fp8bOut::kGlu)
-    store_glu<S>(c, acc, t, sub0, tn);
+    n = store_glu<S>(c, acc, t, sub0, tn);
   else if constexpr (kOut == Fp8bOut::kGluGrad)
-    store_grad<S>(c, acc, t, sub0, tn);
+    n = store_grad<S>(c, acc, t, sub0, tn);
   else
-    store_sums<S, kOut == Fp8bOut::kFp32>(c, acc, t, sub0, tn);
+    n = store_sums<S, kOut == Fp8bOut::kFp32>(c, acc, t, sub0, tn);
+  stored(at, n);
 }
 
 template <Fp8bOut kOut>
@@ -680,8 +737,8 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     for (int u = 0; u < kLoads; ++u) issue(c, k, p, half_at(c, 2 * p), half_at(c, 2 * p + 1), u);
     advance(c, k);
   }
-  publish();
-  Place at{0, 0, 4};
+  wait_and_meet<kLoads + 2>();  // stage 0 but for its second half
+  Place at{0, 0, 4, 0, 0};
   for (int i = 0; i < mine; ++i) {
     // as the cursor noted it
     const v4u info = lds_v4(c.lds + kInfo + 128 * wave + 16 * (i & 7));
