@@ -2,20 +2,27 @@
 // dw[e, n, k] = sum over the rows s of group e of dy[s, n] x[r(s), k].
 //
 // The sum runs over rows, along which both scales vary, so the products are made
-// in the bf16 matrix cores.  x's codes are exact in bf16; dy's codes are
-// multiplied by both scales and rounded once (by at most 2^-8 of each product),
-// for each of the tile's two blocks of k.
+// in the fp16 matrix cores (the rate of bf16, three bits more).  x's codes are
+// exact in fp16; dy's codes are multiplied by both scales, once for each of the
+// tile's two blocks of k.  The scales' products are divided first by a power of two
+// that brings the largest of the group's rows to [2^4, 2^6), so that the range of
+// fp16 costs nothing: a product's two roundings, of the scale and of the product, are
+// 2^-10 of it, and for rows whose scales are 2^-20 of the largest and less 2^-31 of
+// that.  The sums are fp32.
 //
 // A workgroup makes 256 x 256 outputs of one expert, eight waves of 64 x 128 by
-// v_mfma_f32_32x32x16_bf16, in steps of 32 rows.  The matrix cores want eight
+// v_mfma_f32_32x32x16_f16, in steps of 32 rows.  The matrix cores want eight
 // neighbouring rows of one column in a lane: a thread reads four bytes of eight
-// rows each, and the conversion of pairs of rows to bf16 is the transposition.
-// Waves 0-3 convert dy, waves 4-7 x.  LDS holds [eight rows][column c of four]
-// [group of four columns], 16 bytes each, so that writes and reads run along
-// neighbouring addresses; a lane ends with four neighbouring outputs.
+// rows each, converts them to pairs of columns and swaps halves to pairs of rows.
+// Waves 0-3 convert dy, waves 4-7 x, each between its MFMAs; a SIMD has one of
+// either.  LDS holds [eight rows][column c of four][group of four columns], 16 bytes
+// each, so that writes and reads run along neighbouring addresses; a lane ends with
+// four neighbouring outputs.
 //
 // Where the tiles are fewer than the CUs, the rows are split; the parts' sums go
 // through memory in fp32 and are added in the order of the rows.
+#include <type_traits>
+
 #include "fp8b.h"
 #include "tiled.h"
 
@@ -34,8 +41,14 @@ struct GradLaunch {
   float* partial;   // their sums, where there are several
 };
 
-__device__ __forceinline__ v16f mfma_bf16(v4u a, v4u b, v16f c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ v16f mfma_f16(v4u a, v4u b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t mul_pair(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, a) * __builtin_bit_cast(v2h, b));
 }
 
 constexpr int kRing = 3;    // steps whose rows and scales are in registers or on their way
@@ -44,7 +57,7 @@ constexpr int kPanel8 = 8;  // k tiles of a panel
 template <bool kF32, bool kGather>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void grad_kernel(GradLaunch g) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuf];
-  __shared__ __attribute__((aligned(16))) float scl[2][4][kStepRows];  // dy's scale x x's: [n block][k block]
+  __shared__ __attribute__((aligned(16))) _Float16 scl[2][4][kStepRows];  // the scales' products: [n block][k block]
   const Fp8bGradArgs& a = g.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Workgroup b runs on XCD b % 8, which takes a contiguous eighth of an expert's
@@ -68,85 +81,40 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int steps = (end - begin + kStepRows - 1) / kStepRows;
   auto row_of = [&](int step, int r) { return (int)min((long)begin + (long)kStepRows * step + r, (long)end - 1); };
 
-  // Conversion: this thread's four columns of rows 8 o .. 8 o + 7 of a step.  The
-  // loads of a step go out kRing steps before its conversion, the row indices that
-  // they need kRing steps before that.
-  const bool is_x = wave >= 4;
-  const int o = wave & 3;
-  const int width = is_x ? a.K : a.N;
-  const int col = min(kTile * (is_x ? tk : tn) + 4 * lane, width - 4);  // columns past the last: not stored
-  const uint8_t* codes = (is_x ? a.xq : a.yq) + col;
-  uint32_t raw[kRing][8];
-  int entry[kRing];  // lanes 0 .. 7: x rows of the step's rows 8 o + lane
-  auto load_entries = [&](int step, int slot) {
-    if constexpr (kGather)
-      if (is_x) entry[slot] = entry_row(a.rows, row_of(step, 8 * o + (lane & 7)), a.div, a.X);
-  };
-  auto load_codes = [&](int step, int slot) {
+  // The largest scales of the group's rows in the tile's blocks, as powers of two:
+  // y_exp and x_exp with scale < 2^exp.
+  const int nb0 = min(2 * tn, a.N / 128 - 1), nb1 = min(2 * tn + 1, a.N / 128 - 1);
+  const int kb0 = min(2 * tk, a.K / 128 - 1), kb1 = min(2 * tk + 1, a.K / 128 - 1);
+  auto x_row = [&](int s) { return kGather ? entry_row(a.rows, s, a.div, a.X) : s; };
+  int y_exp[2], x_exp[2];
+  {
+    const float* p[4] = {a.ys + (size_t)nb0 * a.P, a.ys + (size_t)nb1 * a.P, a.xs + (size_t)kb0 * a.X,
+                         a.xs + (size_t)kb1 * a.X};
+    float top[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = begin + tid; s < end; s += 512) {
+      const int x = x_row(s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int s = row_of(step, 8 * o + i);
-      if constexpr (kGather)
-        if (is_x) s = __builtin_amdgcn_readlane(entry[slot], i);
-      raw[slot][i] = *reinterpret_cast<const uint32_t*>(codes + (size_t)s * width);
+      for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], fabsf(p[i][i < 2 ? s : x]));
     }
-  };
-  // scales: threads 0 .. 127, one product each
-  const int sn = (tid >> 6) & 1, sk = (tid >> 5) & 1, sr = tid & 31;
-  const int nb = min(2 * tn + sn, a.N / 128 - 1), kb = min(2 * tk + sk, a.K / 128 - 1);
-  const float* ys = a.ys + (size_t)nb * a.P;
-  const float* xs = a.xs + (size_t)kb * a.X;
-  float fy[kRing], fx[kRing];
-  int fentry[kRing];
-  auto load_scale_entries = [&](int step, int slot) {
-    if constexpr (kGather)
-      if (wave < 2) fentry[slot] = entry_row(a.rows, row_of(step, sr), a.div, a.X);
-  };
-  auto load_scales = [&](int step, int slot) {
-    if (wave < 2) {
-      const int s = row_of(step, sr);
-      fy[slot] = ys[s];
-      fx[slot] = xs[kGather ? fentry[slot] : s];
+    __shared__ float tops[8][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float m = max_lanes_xor16_32(row16_max(top[i]));
+      if (lane == 0) tops[wave][i] = m;
     }
-  };
-  auto put_scales = [&](int step, int slot) {
-    if (wave < 2) scl[step & 1][2 * sn + sk][sr] = begin + kStepRows * (long)step + sr < end ? fy[slot] * fx[slot] : 0.0f;
-  };
-  auto convert = [&](int step, int slot) {
-    uint8_t* buf = lds + (step & 1) * kBuf;
-    float v[8][4];
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[slot][i], false);
-      const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[slot][i], true);
-      v[i][0] = lo[0], v[i][1] = lo[1], v[i][2] = hi[0], v[i][3] = hi[1];
+    for (int i = 0; i < 4; ++i) {
+      float m = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) m = fmaxf(m, tops[w][i]);
+      const int exp = (int)wave_u32((uint32_t)__builtin_amdgcn_frexp_expf(m));
+      (i < 2 ? y_exp[i & 1] : x_exp[i & 1]) = exp;
     }
-    auto put = [&](uint8_t* panel, const float (&k)[8], bool scaled) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        v4u w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = scaled ? f32x2_to_bf16(v[2 * i][c] * k[2 * i], v[2 * i + 1][c] * k[2 * i + 1])
-                        : f32x2_to_bf16(v[2 * i][c], v[2 * i + 1][c]);
-        *reinterpret_cast<v4u*>(panel + (o * kTile + c * 64 + lane) * 16) = w;
-      }
-    };
-    if (is_x) {
-      const float none[8] = {};
-      put(buf + 2 * kPanel, none, false);
-    } else {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const float* p = &scl[step & 1][2 * (lane >> 5) + b][8 * o];
-        const v4f k0 = *reinterpret_cast<const v4f*>(p), k1 = *reinterpret_cast<const v4f*>(p + 4);
-        const float k[8] = {k0[0], k0[1], k0[2], k0[3], k1[0], k1[1], k1[2], k1[3]};
-        put(buf + b * kPanel, k, true);
-      }
-    }
-  };
+  }
+  constexpr int kUp = 6;  // the scales' products are brought below 2^kUp, times 448 below 2^15
 
-  // products: n rows 4 q + c for q of half wn % 2, c = 2 (wn / 2) + {0, 1}; k columns of block wk
+  // products: n rows 4 q + c for q of half wn % 2 (block wn % 2), c = 2 (wn / 2) + {0, 1}; k columns of block wk
   const int wn = wave >> 1, wk = wave & 1, r = lane & 31, h = lane >> 5;
   v16f acc[2][4];
 #pragma unroll
@@ -155,37 +123,119 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  // Step j: its products from one buffer while step j + 1 is converted into the
-  // other; put_scales(j + 2), which the next step's conversion reads.  Loads past
-  // the last step read its rows again.
-  auto iterate = [&](int j, int slot) {  // slot: (j + 1) % kRing
-    const uint8_t* buf = lds + (j & 1) * kBuf;
-    const uint8_t* pa = buf + wk * kPanel + (size_t)(128 * (wn >> 1) + 32 * (wn & 1) + r) * 16;
-    const uint8_t* pb = buf + 2 * kPanel + (size_t)(32 * wk + r) * 16;
-    convert(j + 1, slot);
-    load_codes(j + 1 + kRing, slot);
-    load_entries(j + 1 + 2 * kRing, slot);
+
+  // The loop of a wave that converts x (kIsX) or dy: four columns a thread of rows
+  // 8 o .. 8 o + 7 of a step.  The loads of a step go out kRing steps before its
+  // conversion, the row indices that they need kRing steps before that.
+  auto run = [&](auto is_x) {
+    constexpr bool kIsX = decltype(is_x)::value, kIndexed = kIsX && kGather;
+    const int o = wave & 3;
+    const int width = kIsX ? a.K : a.N;
+    const int col = min(kTile * (kIsX ? tk : tn) + 4 * lane, width - 4);  // columns past the last: not stored
+    const uint8_t* codes = (kIsX ? a.xq : a.yq) + col;
+    uint32_t raw[kRing][8];
+    int entry[kRing];  // lanes 0 .. 7: x rows of the step's rows 8 o + lane
+    auto load_entries = [&](int step, int slot) {
+      if constexpr (kIndexed) entry[slot] = x_row(row_of(step, 8 * o + (lane & 7)));
+    };
+    auto load_codes = [&](int step, int slot) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {  // 16 rows
-      const size_t at = (size_t)((2 * u + h) * kTile) * 16;
+      for (int i = 0; i < 8; ++i) {
+        const int s = kIndexed ? __builtin_amdgcn_readlane(entry[slot], i) : row_of(step, 8 * o + i);
+        raw[slot][i] = *reinterpret_cast<const uint32_t*>(codes + (size_t)s * width);
+      }
+    };
+    // scales: a dy wave one k block and n block each (two waves an n block), for 32 rows; its lanes' upper half idles
+    const int sn = o >> 1, sk = o & 1, sr = lane & 31;
+    const float* ys = a.ys + (size_t)(sn ? nb1 : nb0) * a.P;
+    const float* xs = a.xs + (size_t)(sk ? kb1 : kb0) * a.X;
+    const int up_y = -y_exp[sn], up_x = kUp - x_exp[sk];
+    float fy[kRing], fx[kRing];
+    int fentry[kRing];
+    auto load_scale_entries = [&](int step, int slot) {
+      if constexpr (!kIsX && kGather) fentry[slot] = x_row(row_of(step, sr));
+    };
+    auto load_scales = [&](int step, int slot) {
+      if constexpr (!kIsX) {
+        const int s = row_of(step, sr);
+        fy[slot] = ys[s];
+        fx[slot] = xs[kGather ? fentry[slot] : s];
+      }
+    };
+    auto put_scales = [&](int step, int slot) {
+      if constexpr (!kIsX) {
+        const float k = __builtin_amdgcn_ldexpf(fy[slot], up_y) * __builtin_amdgcn_ldexpf(fx[slot], up_x);
+        scl[step & 1][2 * sn + sk][sr] = (_Float16)(begin + kStepRows * (long)step + sr < end ? k : 0.0f);
+      }
+    };
+    // a step's conversion in pieces: rows to fp16, then each column (and block of k)
+    uint32_t v[8][2], k[2][4];
+    auto rows_to_half = [&](int step, int slot) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+          v[i][d] = __builtin_bit_cast(
+              uint32_t, d ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)raw[slot][i], 1.0f, true)
+                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)raw[slot][i], 1.0f, false));
+      if constexpr (!kIsX) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const v4u t = *reinterpret_cast<const v4u*>(&scl[step & 1][2 * (lane >> 5) + b][8 * o]);
+          k[b][0] = t.x, k[b][1] = t.y, k[b][2] = t.z, k[b][3] = t.w;
+        }
+      }
+    };
+    auto put_column = [&](int step, int c) {
+      uint8_t* to = lds + (step & 1) * kBuf + (kIsX ? 2 * kPanel : 0) + (o * kTile + c * 64 + lane) * 16;
+      v4u w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // halves c % 2 of rows 2 i and 2 i + 1
+        w[i] = __builtin_amdgcn_perm(v[2 * i + 1][c >> 1], v[2 * i][c >> 1], c & 1 ? 0x07060302u : 0x05040100u);
+      if constexpr (kIsX) {
+        *reinterpret_cast<v4u*>(to) = w;
+      } else {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          *reinterpret_cast<v4u*>(to + b * kPanel) =
+              v4u{mul_pair(w[0], k[b][0]), mul_pair(w[1], k[b][1]), mul_pair(w[2], k[b][2]), mul_pair(w[3], k[b][3])};
+      }
+    };
+    // Step j: its products from one buffer while step j + 1 is converted into the
+    // other; put_scales(j + 2), which the next step's conversion reads.  Loads past
+    // the last step read its rows again.
+    auto iterate = [&](int j, int slot) {  // slot: (j + 1) % kRing
+      const uint8_t* buf = lds + (j & 1) * kBuf;
+      const uint8_t* pa = buf + wk * kPanel + (size_t)(128 * (wn >> 1) + 32 * (wn & 1) + r) * 16;
+      const uint8_t* pb = buf + 2 * kPanel + (size_t)(32 * wk + r) * 16;
       v4u fa[2], fb[4];
+      auto read_a = [&](int u, int i) { fa[i] = *reinterpret_cast<const v4u*>(pa + ((2 * u + h) * kTile + 64 * i) * 16); };
+      auto read_b = [&](int u, int c) { fb[c] = *reinterpret_cast<const v4u*>(pb + ((2 * u + h) * kTile + 64 * c) * 16); };
 #pragma unroll
-      for (int i = 0; i < 2; ++i) fa[i] = *reinterpret_cast<const v4u*>(pa + at + 64 * 16 * i);
+      for (int i = 0; i < 2; ++i) read_a(0, i);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) fb[c] = *reinterpret_cast<const v4u*>(pb + at + 64 * 16 * c);
+      for (int c = 0; c < 4; ++c) read_b(0, c);
+      rows_to_half(j + 1, slot);
+      load_codes(j + 1 + kRing, slot);
+      load_entries(j + 1 + 2 * kRing, slot);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][c] = mfma_bf16(fa[i], fb[c], acc[i][c]);
-    }
-    const int next = (slot + 1) % kRing;
-    put_scales(j + 2, next);
-    load_scales(j + 2 + kRing, next);
-    load_scale_entries(j + 2 + 2 * kRing, next);
-    // (not __syncthreads, which would wait for the loads of the steps to come)
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  };
-  if (steps > 0) {
+      for (int m = 0; m < 16; ++m) {
+        const int u = m >> 3, i = (m >> 2) & 1, c = m & 3;
+        acc[i][c] = mfma_f16(fa[i], fb[c], acc[i][c]);
+        // the second 16 rows' fragments, each behind its register's last use
+        if (u == 0 && c == 3) read_a(1, i);
+        if (u == 0 && i == 1) read_b(1, c);
+        if (c == 1) put_column(j + 1, m >> 2);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const int next = (slot + 1) % kRing;
+      put_scales(j + 2, next);
+      load_scales(j + 2 + kRing, next);
+      load_scale_entries(j + 2 + 2 * kRing, next);
+      // (not __syncthreads, which would wait for the loads of the steps to come)
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
 #pragma unroll
     for (int q = 0; q < kRing; ++q) {
       load_entries(q, q);
@@ -205,7 +255,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     load_scale_entries(2 * kRing, 0);
     load_scale_entries(2 * kRing + 1, 1);
     __syncthreads();
-    convert(0, 0);
+    rows_to_half(0, 0);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) put_column(0, c);
     load_codes(kRing, 0);
     load_entries(2 * kRing, 0);
     __syncthreads();
@@ -218,7 +270,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
     if (j < steps) iterate(j, 1);
     if (j + 1 < steps) iterate(j + 1, 2);
+  };
+  if (steps > 0) {
+    if (wave >= 4)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
   }
+  const int down = (wn & 1 ? y_exp[1] : y_exp[0]) + (wk ? x_exp[1] : x_exp[0]) - kUp;
 
   // element v of a lane: row q = 32 (wn % 2) + 8 (v / 4) + 4 h + v % 4, its four columns in the four tiles
   const int k0 = kTile * tk + 128 * wk + 4 * r;
@@ -233,7 +292,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       const int n = kTile * tn + 4 * (32 * (wn & 1) + 8 * (v >> 2) + 4 * h + (v & 3)) + 2 * (wn >> 1) + i;
       if (n >= a.N) continue;
       const size_t at = (size_t)n * a.K + k0;
-      const v4f s = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
+      const v4f s = {__builtin_amdgcn_ldexpf(acc[i][0][v], down), __builtin_amdgcn_ldexpf(acc[i][1][v], down),
+                     __builtin_amdgcn_ldexpf(acc[i][2][v], down), __builtin_amdgcn_ldexpf(acc[i][3][v], down)};
       if (kF32 || g.parts > 1)
         __builtin_nontemporal_store(s, reinterpret_cast<global<v4f>*>((uintptr_t)(sums + at)));
       else

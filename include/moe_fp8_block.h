@@ -167,8 +167,10 @@ moe_status_t moe_fp8_block_glu_backward(const moe_fp8_block_weights_t* w /*(host
 /*
  * Gradient of the weights: dw[e, n, k] = sum over the rows s of group e of
  * dy[s, n] x[r(s), k], both rows quantised.  Their scales vary along this sum,
- * so it runs in the bf16 matrix cores: x's codes are exact there, each
- * dy * (both scales) is rounded to bf16; sums in fp32, rounded once to dw_type
+ * so it runs in the fp16 matrix cores: x's codes are exact there; the scales'
+ * product, relative to the largest of the group's rows, and dy's code times it are
+ * rounded to fp16 (2^-10 of each product together, or 2^-31 of the largest row's
+ * where the scales are below 2^-20 of its); sums in fp32, rounded once to dw_type
  * (bf16, or fp32 as it is).  A group without rows gets zeros.
  *   yq [P, N], ys [N/128, P]; xq [X, K], xs [K/128, X]; codes 16-byte aligned
  *   offsets null: one group of P rows (E == 1); rows as above
