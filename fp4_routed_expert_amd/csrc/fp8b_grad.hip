@@ -51,12 +51,12 @@ __device__ __forceinline__ uint32_t mul_pair(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, a) * __builtin_bit_cast(v2h, b));
 }
 
-constexpr int kRing = 3;    // steps whose rows and scales are in registers or on their way
+constexpr int kRing = 3;    // steps whose rows and scales are in registers or on their way, and steps in LDS
 constexpr int kPanel8 = 8;  // k tiles of a panel
 
 template <bool kF32, bool kGather>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void grad_kernel(GradLaunch g) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuf];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing * kBuf];
   __shared__ __attribute__((aligned(16))) _Float16 scl[2][4][kStepRows];  // the scales' products: [n block][k block]
   const Fp8bGradArgs& a = g.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -79,7 +79,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     begin = first;
   }
   const int steps = (end - begin + kStepRows - 1) / kStepRows;
-  auto row_of = [&](int step, int r) { return (int)min((long)begin + (long)kStepRows * step + r, (long)end - 1); };
+  // row r of a step, past the group its last one
+  auto row_of = [&](int step, int r) { return (int)min((uint32_t)begin + (uint32_t)(kStepRows * step + r), (uint32_t)(end - 1)); };
 
   // The largest scales of the group's rows in the tile's blocks, as powers of two:
   // y_exp and x_exp with scale < 2^exp.
@@ -131,8 +132,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     constexpr bool kIsX = decltype(is_x)::value, kIndexed = kIsX && kGather;
     const int o = wave & 3;
     const int width = kIsX ? a.K : a.N;
-    const int col = min(kTile * (kIsX ? tk : tn) + 4 * lane, width - 4);  // columns past the last: not stored
-    const uint8_t* codes = (kIsX ? a.xq : a.yq) + col;
+    const uint32_t col = (uint32_t)min(kTile * (kIsX ? tk : tn) + 4 * lane, width - 4);  // columns past the last: not stored
+    const uint8_t* codes = kIsX ? a.xq : a.yq;  // (uniform: a row's address is made by the scalar unit)
     uint32_t raw[kRing][8];
     int entry[kRing];  // lanes 0 .. 7: x rows of the step's rows 8 o + lane
     auto load_entries = [&](int step, int slot) {
@@ -142,7 +143,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int s = kIndexed ? __builtin_amdgcn_readlane(entry[slot], i) : row_of(step, 8 * o + i);
-        raw[slot][i] = *reinterpret_cast<const uint32_t*>(codes + (size_t)s * width);
+        raw[slot][i] = *reinterpret_cast<const uint32_t*>(wave_ptr(codes + (size_t)s * (size_t)width) + col);
       }
     };
     // scales: a dy wave one k block and n block each (two waves an n block), for 32 rows; its lanes' upper half idles
@@ -165,19 +166,19 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     auto put_scales = [&](int step, int slot) {
       if constexpr (!kIsX) {
         const float k = __builtin_amdgcn_ldexpf(fy[slot], up_y) * __builtin_amdgcn_ldexpf(fx[slot], up_x);
-        scl[step & 1][2 * sn + sk][sr] = (_Float16)(begin + kStepRows * (long)step + sr < end ? k : 0.0f);
+        scl[step & 1][2 * sn + sk][sr] = (_Float16)((uint32_t)begin + (uint32_t)(kStepRows * step + sr) < (uint32_t)end ? k : 0.0f);
       }
     };
-    // a step's conversion in pieces: rows to fp16, then each column (and block of k)
+    // a step's conversion in pieces: two rows to fp16; the scales; each column
     uint32_t v[8][2], k[2][4];
-    auto rows_to_half = [&](int step, int slot) {
+    auto rows_to_half = [&](int m, int slot) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int d = 0; d < 2; ++d)
-          v[i][d] = __builtin_bit_cast(
-              uint32_t, d ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)raw[slot][i], 1.0f, true)
-                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)raw[slot][i], 1.0f, false));
+      for (int i = 2 * m; i < 2 * m + 2; ++i) {
+        v[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)raw[slot][i], 1.0f, false));
+        v[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)raw[slot][i], 1.0f, true));
+      }
+    };
+    auto get_scales = [&](int step) {
       if constexpr (!kIsX) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -186,8 +187,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         }
       }
     };
-    auto put_column = [&](int step, int c) {
-      uint8_t* to = lds + (step & 1) * kBuf + (kIsX ? 2 * kPanel : 0) + (o * kTile + c * 64 + lane) * 16;
+    auto put_column = [&](int slot, int c) {
+      uint8_t* to = lds + slot * kBuf + (kIsX ? 2 * kPanel : 0) + (o * kTile + c * 64 + lane) * 16;
       v4u w;
 #pragma unroll
       for (int i = 0; i < 4; ++i)  // halves c % 2 of rows 2 i and 2 i + 1
@@ -201,38 +202,41 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
               v4u{mul_pair(w[0], k[b][0]), mul_pair(w[1], k[b][1]), mul_pair(w[2], k[b][2]), mul_pair(w[3], k[b][3])};
       }
     };
-    // Step j: its products from one buffer while step j + 1 is converted into the
-    // other; put_scales(j + 2), which the next step's conversion reads.  Loads past
-    // the last step read its rows again.
-    auto iterate = [&](int j, int slot) {  // slot: (j + 1) % kRing
-      const uint8_t* buf = lds + (j & 1) * kBuf;
-      const uint8_t* pa = buf + wk * kPanel + (size_t)(128 * (wn >> 1) + 32 * (wn & 1) + r) * 16;
-      const uint8_t* pb = buf + 2 * kPanel + (size_t)(32 * wk + r) * 16;
-      v4u fa[2], fb[4];
-      auto read_a = [&](int u, int i) { fa[i] = *reinterpret_cast<const v4u*>(pa + ((2 * u + h) * kTile + 64 * i) * 16); };
-      auto read_b = [&](int u, int c) { fb[c] = *reinterpret_cast<const v4u*>(pb + ((2 * u + h) * kTile + 64 * c) * 16); };
-#pragma unroll
-      for (int i = 0; i < 2; ++i) read_a(0, i);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) read_b(0, c);
-      rows_to_half(j + 1, slot);
-      load_codes(j + 1 + kRing, slot);
-      load_entries(j + 1 + 2 * kRing, slot);
-      __builtin_amdgcn_sched_barrier(0);
+    // fragments of 16 rows u of the step in a buffer
+    v4u fa[2], fb[4];
+    const uint8_t* pa = lds + wk * kPanel + (h * kTile + 128 * (wn >> 1) + 32 * (wn & 1) + r) * 16;
+    const uint8_t* pb = lds + 2 * kPanel + (h * kTile + 32 * wk + r) * 16;
+    auto read_a = [&](int slot, int u, int i) {
+      fa[i] = *reinterpret_cast<const v4u*>(pa + slot * kBuf + (2 * u * kTile + 64 * i) * 16);
+    };
+    auto read_b = [&](int slot, int u, int c) {
+      fb[c] = *reinterpret_cast<const v4u*>(pb + slot * kBuf + (2 * u * kTile + 64 * c) * 16);
+    };
+    // Step j, j % kRing = slot: its products, while step j + 2 is converted into the
+    // buffer of step j - 1 and the scales of step j + 3 go to LDS; a fragment's
+    // registers take its successor's (at the end the next step's, which the last
+    // barrier has published) behind their last use.  Loads past the last step read
+    // its rows again.
+    auto iterate = [&](int j, int slot) {
+      const int next = (slot + 1) % kRing, to = (slot + 2) % kRing;
 #pragma unroll
       for (int m = 0; m < 16; ++m) {
         const int u = m >> 3, i = (m >> 2) & 1, c = m & 3;
         acc[i][c] = mfma_f16(fa[i], fb[c], acc[i][c]);
-        // the second 16 rows' fragments, each behind its register's last use
-        if (u == 0 && c == 3) read_a(1, i);
-        if (u == 0 && i == 1) read_b(1, c);
-        if (c == 1) put_column(j + 1, m >> 2);
+        if (c == 3) read_a(u ? next : slot, 1 - u, i);
+        if (i == 1) read_b(u ? next : slot, 1 - u, c);
+        if (m < 4) rows_to_half(m, to);
+        if (m == 2) get_scales(j + 2);
+        if (m == 4) {
+          load_codes(j + 2 + kRing, to);
+          load_entries(j + 2 + 2 * kRing, to);
+        }
+        if (m >= 5 && m % 3 == 2) put_column(to, (m - 5) / 3);
         __builtin_amdgcn_sched_barrier(0);
       }
-      const int next = (slot + 1) % kRing;
-      put_scales(j + 2, next);
-      load_scales(j + 2 + kRing, next);
-      load_scale_entries(j + 2 + 2 * kRing, next);
+      put_scales(j + 3, slot);
+      load_scales(j + 3 + kRing, slot);
+      load_scale_entries(j + 3 + 2 * kRing, slot);
       // (not __syncthreads, which would wait for the loads of the steps to come)
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     };
@@ -250,26 +254,38 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
     put_scales(0, 0);
     put_scales(1, 1);
-    load_scales(kRing, 0);
-    load_scales(kRing + 1, 1);
-    load_scale_entries(2 * kRing, 0);
-    load_scale_entries(2 * kRing + 1, 1);
     __syncthreads();
-    rows_to_half(0, 0);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) put_column(0, c);
-    load_codes(kRing, 0);
-    load_entries(2 * kRing, 0);
+    for (int q = 0; q < 2; ++q) {
+      get_scales(q);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) rows_to_half(m, q);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) put_column(q, c);
+      load_codes(kRing + q, q);
+      load_entries(2 * kRing + q, q);
+    }
     __syncthreads();
-    // (the last step converts one that does not exist, whose scales are zeros)
+    put_scales(2, 2);
+#pragma unroll
+    for (int q = 0; q < kRing; ++q) {
+      load_scales(kRing + q, q);
+      load_scale_entries(2 * kRing + q, q);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) read_a(0, 0, i);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) read_b(0, 0, c);
+    __syncthreads();
+    // (the last steps convert ones that do not exist, whose scales are zeros)
     int j = 0;
     for (; j + kRing <= steps; j += kRing) {
-      iterate(j, 1);
-      iterate(j + 1, 2);
-      iterate(j + 2, 0);
+      iterate(j, 0);
+      iterate(j + 1, 1);
+      iterate(j + 2, 2);
     }
-    if (j < steps) iterate(j, 1);
-    if (j + 1 < steps) iterate(j + 1, 2);
+    if (j < steps) iterate(j, 0);
+    if (j + 1 < steps) iterate(j + 1, 1);
   };
   if (steps > 0) {
     if (wave >= 4)
