@@ -41,15 +41,35 @@ moe_status_t check_weights(const moe_fp8_block_weights_t* w, int32_t glu) {
 // The tiled product addresses activation rows by 32-bit byte offsets.
 bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 << 32) - 4096; }
 
-// 0: stream the weights, 1: tiled, -1: bad flags.
-constexpr int64_t kStreamRows = 16, kStreamPasses = 1024;
-int choose_path(int64_t P, const Fp8bLayout& L, uint32_t flags) {
+// 0: stream the weights, 1: tiled, -1: bad flags.  By default the weights are
+// streamed while the groups average at most 12 rows (us, streaming against tiled, 64
+// experts: SwiGLU K 4096 N 1536, 6 rows 119 and 142, 12 rows 145 and 146, 24 rows 181
+// and 148; 256 experts, K 7168 N 2048, 8 rows 1202 and 1277, 16 rows 1830 and 1320),
+// for the backward call, whose rows take a second launch then, at most 6 (K 4096 N
+// 2048, 6 rows 99 and 100, 12 rows 125 and 103), or while streaming makes at most 2048
+// passes of 32 rows over a weight tile, eight per CU: the tiled product has few items
+// then.  Dense: K 4096 N 1536, 512 rows (1536 passes) 20 and 27, 768 rows (2304) 30
+// and 27; K 16384 N 7168, 128 rows (1792) 100 and 119, 160 rows (2240) 125 and 116; K
+// 7168 N 2048, 512 rows (2048) 42 and 42.  Where the sums stay in fp32 up to 3328: K
+// 16384 N 7168, 192 rows (2688) 161 and 186, 256 rows (3584) 197 and 185; K 1536 N
+// 4096, 512 rows (4096) 21 and 24.  Grouped, where the tiled product lists its tiles
+// first, up to 2400 (a group's last pass counted half): 8 experts, K 512 N 512, 2048
+// rows (2176) 7.4 and 11.8; 16 experts, K 2048 N 512, 2000 rows (2240) 20 and 20; 30
+// experts, K 1024 N 1024, 1000 rows (2944) 14 and 14; 8 experts, K 4096 N 4096, 512
+// rows (5120) 67 and 32.
+// The averages do not see skew, which only the device knows: streaming walks a
+// group's rows 16 or 32 at a time, by one workgroup per tile pair once the groups'
+// tiles fill the CUs.  A caller that knows its routing to be skewed forces the tiled
+// product.
+int choose_path(int64_t P, const Fp8bLayout& L, Fp8bOut out, bool grouped, uint32_t flags) {
   const bool fd = flags & MOE_FLAG_FORCE_DECODE, fp = flags & MOE_FLAG_FORCE_PREFILL;
   if ((flags & ~(MOE_FLAG_FORCE_DECODE | MOE_FLAG_FORCE_PREFILL)) != 0 || (fd && fp)) return -1;
   if (fd) return 0;
   if (fp) return 1;
-  const int64_t passes = P / 32 + (L.E + 1) / 2;
-  return P <= kStreamRows * L.E || passes * L.NT <= kStreamPasses ? 0 : 1;
+  const int64_t rows = out == Fp8bOut::kGluGrad ? 6 : 12;
+  const int64_t most = out == Fp8bOut::kFp32 ? 3328 : grouped ? 2400 : 2048;
+  const int64_t passes = grouped ? P / 32 + (L.E + 1) / 2 : (P + 31) / 32;
+  return P <= rows * L.E || passes * L.NT <= most ? 0 : 1;
 }
 
 size_t tiled_bytes(int32_t P, int32_t E) { return PackedLayout::align256(fp8b_tiled_ws_bytes(P, E)); }
@@ -62,7 +82,7 @@ size_t rows_bytes(int32_t P, const Fp8bLayout& L, int path) {
 // One size for the forward and the backward call, which may take different paths (twice the tiles with gate and up).
 size_t glu_bytes(int32_t P, int32_t E, int32_t N, int32_t K, uint32_t flags) {
   const Fp8bLayout one(E, N, K, false), two(E, N, K, true);
-  const int p1 = choose_path(P, one, flags), p2 = choose_path(P, two, flags);
+  const int p1 = choose_path(P, one, Fp8bOut::kGluGrad, true, flags), p2 = choose_path(P, two, Fp8bOut::kGlu, true, flags);
   if (p1 < 0 || p2 < 0) return 0;
   const size_t a = rows_bytes(P, one, p1), b = rows_bytes(P, two, p2);
   return a > b ? a : b;
@@ -115,7 +135,7 @@ moe_status_t gated(const moe_fp8_block_weights_t* w, Fp8bOut out, const uint8_t*
   if (st != MOE_OK) return st;
   if (P < 0 || X < 0 || row_div < 1) return MOE_ERR_INVALID_ARGUMENT;
   const Fp8bLayout L(w->E, w->N, w->K, w->glu != 0);
-  const int path = choose_path(P, L, flags);
+  const int path = choose_path(P, L, out, true, flags);
   if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
   if (w->N % 128 != 0 || rows_too_large(X, w->K) || P > kMaxP) return MOE_ERR_UNSUPPORTED;
   if (P == 0) return MOE_OK;
@@ -176,14 +196,15 @@ moe_status_t moe_fp8_block_dense_forward(const moe_fp8_block_weights_t* w, const
   if (st != MOE_OK) return st;
   if (w->E != 1 || T < 0 || !sum_type(y_type)) return MOE_ERR_INVALID_ARGUMENT;
   const Fp8bLayout L(1, w->N, w->K, false);
-  const int path = choose_path(T, L, flags);
+  const Fp8bOut out = y_type == MOE_TYPE_FP32 ? Fp8bOut::kFp32 : Fp8bOut::kBf16;
+  const int path = choose_path(T, L, out, false, flags);
   if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
   if (rows_too_large(T, w->K) || T > kMaxP) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!xq || !xs || !y || !aligned(xq, 16) || !aligned(xs, 4) || !aligned(y, 16)) return MOE_ERR_INVALID_ARGUMENT;
   const Fp8bArgs a{static_cast<const uint8_t*>(w->packed), xq, xs, T, nullptr, nullptr, 1, T, y, nullptr, nullptr,
                    nullptr, nullptr};
-  return run(a, L, path, y_type == MOE_TYPE_FP32 ? Fp8bOut::kFp32 : Fp8bOut::kBf16, nullptr, stream);
+  return run(a, L, path, out, nullptr, stream);
 }
 
 size_t moe_fp8_block_grouped_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K) {
@@ -199,7 +220,8 @@ moe_status_t moe_fp8_block_grouped_forward(const moe_fp8_block_weights_t* w, con
   if (st != MOE_OK) return st;
   if (P < 0 || X < 0 || row_div < 1 || !sum_type(y_type)) return MOE_ERR_INVALID_ARGUMENT;
   const Fp8bLayout L(w->E, w->N, w->K, false);
-  const int path = choose_path(P, L, flags);
+  const Fp8bOut out = y_type == MOE_TYPE_FP32 ? Fp8bOut::kFp32 : Fp8bOut::kBf16;
+  const int path = choose_path(P, L, out, true, flags);
   if (path < 0) return MOE_ERR_INVALID_ARGUMENT;
   if (rows_too_large(X, w->K) || P > kMaxP) return MOE_ERR_UNSUPPORTED;
   if (P == 0) return MOE_OK;
@@ -211,7 +233,7 @@ moe_status_t moe_fp8_block_grouped_forward(const moe_fp8_block_weights_t* w, con
   if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
   const Fp8bArgs a{static_cast<const uint8_t*>(w->packed), xq, xs, X, offsets, rows, row_div, P, y, nullptr, nullptr,
                    nullptr, nullptr};
-  return run(a, L, path, y_type == MOE_TYPE_FP32 ? Fp8bOut::kFp32 : Fp8bOut::kBf16, workspace, stream);
+  return run(a, L, path, out, workspace, stream);
 }
 
 size_t moe_fp8_block_glu_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K, uint32_t flags) {

@@ -196,16 +196,37 @@ void stream_as(const Fp8bArgs& a, const Fp8bLayout& L, hipStream_t st) {
   hipLaunchKernelGGL((stream_kernel<NW, NT, TT, kB, kOut>), grid, dim3(64 * NW), 0, st, a, L);
 }
 
+// What a launch's workgroups look like, by the rows of a group on average and by
+// how many tiles there are (us; weights not in any cache):
+// - Up to 16 rows, tiles at most one per CU: one tile each, by 16 waves.  K 4096, N
+//   1536, 8 rows (96 tiles): 5.1 against 6.2 with pairs by four waves; K 7168, N
+//   2048 (128 tiles): 7.0 and 9.2.
+// - Up to 16 rows, more tiles: pairs, by four waves with four K-steps each in
+//   flight.  K 16384, N 7168, 8 rows (448 tiles): 19.7 against 23.8 with single tiles
+//   by 16 waves, 21.5 with pairs by eight; SwiGLU, 64 experts, K 4096, N 1536, 48
+//   rows: 63.8 and, by 16 waves, 81.  Pairs of gate and up are one per CU: 16 waves.
+// - More rows: two token tiles to a pass over a pair, by eight waves.  K 16384, N
+//   7168, 32 rows: 27 against 30 with four waves; K 7168, N 2048, 256 rows: 23 and 23.
+//   With exact products (whose operands take more registers) and more pairs than
+//   CUs by four: K 4096, N 1536, 333 rows 18 against 21.
+// The counts are against the 256 CUs that these were measured on; a device with
+// fewer gets the same results.
 template <Fp8bOut kOut>
 void stream_for(const Fp8bArgs& a, const Fp8bLayout& L, hipStream_t st) {
   constexpr bool kGlu = kOut == Fp8bOut::kGlu;
-  const bool two = a.P > 16 * (a.offsets ? L.E : 1);
-  if (two)
-    stream_as<8, 2, 2, 2, kOut>(a, L, st);
-  else if (kGlu || L.NT > 512)
-    stream_as<8, 2, 1, 2, kOut>(a, L, st);
-  else
+  constexpr long kCUs = 256;
+  const long groups = a.offsets ? min((long)L.E, (long)a.P) : 1;
+  if (a.P > 16 * groups) {
+    const long passes = a.offsets ? groups : (a.P + 31) / 32;
+    if (kOut == Fp8bOut::kFp32 && passes * L.NT > 2 * kCUs)
+      stream_as<4, 2, 2, 2, kOut>(a, L, st);
+    else
+      stream_as<8, 2, 2, 2, kOut>(a, L, st);
+  } else if (groups * L.NT > (kGlu ? 2 : 1) * kCUs) {
+    stream_as<4, 2, 1, 4, kOut>(a, L, st);
+  } else {
     stream_as<16, kGlu ? 2 : 1, 1, 2, kOut>(a, L, st);
+  }
 }
 
 }  // namespace
