@@ -137,6 +137,7 @@ struct Launch {
   const int32_t* ws;     // tile list (grouped)
   const int32_t* xrows;  // x row of each sorted row, or null: the same row
   int tiles, height;     // one group: row tiles and their height
+  int panels;            // of the walk
 };
 typedef __attribute__((address_space(4))) const Launch claunch;
 
@@ -163,7 +164,7 @@ __device__ __forceinline__ void next_item(const claunch* g, Walk& k) {
     k.off -= k.w;
     ++k.tt;
   }
-  if (k.tt >= k.ntt) locate(k);
+  if (k.tt >= k.ntt) locate(k, g->panels);
   look_up(g, k);
 }
 
@@ -722,7 +723,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
     mine = (walk.hi - walk.p + walk.stride - 1) / walk.stride;
     walk.count = 0;
     walk.more = 1;
-    locate(walk);
+    locate(walk, g->panels);
     look_up(g, walk);
     fetch_rows(c, walk);
     wait_vmcnt<0>();
@@ -780,7 +781,7 @@ size_t fp8b_tiled_ws_bytes(long P, int E) { return rows_at(P, E) + 4 * (size_t)P
 hipError_t launch_fp8b_tiled(const Fp8bArgs& a, const Fp8bLayout& L, Fp8bOut out, void* ws, hipStream_t st) {
   const int ntn = (L.NT + kBT - 1) / kBT;
   const int most = out == Fp8bOut::kFp32 ? kWideSubs : 4;
-  Launch g{a, L, nullptr, nullptr, 0, 0};
+  Launch g{a, L, nullptr, nullptr, 0, 0, a.offsets && a.P <= kBM * (long)L.E ? 1 : 4};
   if (a.offsets) {
     int32_t* list = static_cast<int32_t*>(ws);
     int32_t* xrows = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + rows_at(a.P, L.E));

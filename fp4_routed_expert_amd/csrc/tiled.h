@@ -58,7 +58,7 @@ __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t
 }
 
 // Where a wave's walk over the items stands (in LDS between items).  The items
-// go by panels of a quarter of the columns, row tiles running inside a panel,
+// go by panels of columns (a quarter of them), row tiles running inside a panel,
 // so that the items that an XCD holds at one time share rows and weights in
 // its L2.  Steps inside a panel need no division.
 struct Walk {
@@ -72,8 +72,8 @@ struct Walk {
 };
 static_assert(sizeof(Walk) == 64, "four 128-bit words");
 
-__device__ __forceinline__ void locate(Walk& k) {
-  const int sn = (k.ntn + 3) / 4, sc = k.p / (k.ntt * sn), q = k.p - sc * (k.ntt * sn);
+__device__ __forceinline__ void locate(Walk& k, int panels = 4) {
+  const int sn = (k.ntn + panels - 1) / panels, sc = k.p / (k.ntt * sn), q = k.p - sc * (k.ntt * sn);
   k.base = sc * sn;
   k.w = max(min(sn, k.ntn - k.base), 1);
   k.tt = q / k.w;
