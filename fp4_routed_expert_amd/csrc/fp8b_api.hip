@@ -279,7 +279,7 @@ moe_status_t moe_fp8_block_weight_grad(const uint8_t* yq, const float* ys, const
       return MOE_ERR_INVALID_ARGUMENT;
   }
   const size_t need = PackedLayout::align256(fp8b_grad_ws_bytes(P, E, N, K));
-  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (P > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
   // without rows nothing is read: dw is zeros
   const Fp8bGradArgs a{yq, ys, xq, xs, X, P > 0 ? offsets : nullptr, rows, row_div, P, E, N, K, dw};
