@@ -228,7 +228,6 @@ __device__ __forceinline__ void run_rows(const GradCtx& g, v16f (&acc)[2][4]) {
     each([&](auto at) __attribute__((always_inline)) {
       constexpr int m = decltype(at)::value, u = m >> 3, i = (m >> 2) & 1, c = m & 3;
       acc[i][c] = mfma_f16(fa[i], fb[c], acc[i][c]);
-      __builtin_amdgcn_sched_barrier(0);
       if (m == 0) {
         get_codes(slot);
         get_products(j + 1);
@@ -247,7 +246,7 @@ __device__ __forceinline__ void run_rows(const GradCtx& g, v16f (&acc)[2][4]) {
       }
       if (u == 1 && i == 1) read_b(j + 1, 0, c);
       if (m == 15) read_a(j + 1, 0, 1);
-      __builtin_amdgcn_sched_barrier(0);
+      if (c == 3) __builtin_amdgcn_sched_barrier(0);  // (four MFMAs at a time are the compiler's to order)
     }, std::make_integer_sequence<int, 16>{});
   };
   // the first steps' codes, scales and (by plain loads) indices
