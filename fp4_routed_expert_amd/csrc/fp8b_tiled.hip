@@ -501,6 +501,7 @@ __device__ __forceinline__ void step(Ctx& c, Cursor& k, Addr& ad, Place& at, v4f
   at.load = next_half(load1);
 }
 
+__device__ __forceinline__ void store16(void* p, v4u v) { *reinterpret_cast<global<v4u>*>((uintptr_t)p) = v; }
 __device__ __forceinline__ void nt_store16(void* p, v4u v) {
   __builtin_nontemporal_store(v, reinterpret_cast<global<v4u>*>((uintptr_t)p));
 }
@@ -509,8 +510,8 @@ __device__ __forceinline__ void nt_store8(void* p, uint32_t a, uint32_t b) {
 }
 
 // Sums as they are: a lane's pair of tiles is eight neighbouring columns of its
-// token, a quad of lanes (g = 0..3) 32.  The stores are non-temporal: the outputs
-// would push rows and weights out of L2.
+// token, a quad of lanes (g = 0..3) 32.  (Non-temporal stores were 2 % slower: 16
+// experts of 8192 rows, K 2048, N 7168: 1886 us, 1936 with them.)
 template <int S, bool kF32>
 __device__ __forceinline__ int store_sums(const Ctx& c, const v4f (&acc)[8][4], const Tile& t, int sub0, int tn) {
   constexpr size_t kB = kF32 ? 4 : 2;
@@ -527,11 +528,11 @@ __device__ __forceinline__ int store_sums(const Ctx& c, const v4f (&acc)[8][4], 
           const v4f lo = acc[2 * p][i], hi = acc[2 * p + 1][i];
           uint8_t* o = y + ((size_t)(16 * i) * N + 32 * p) * kB;
           if constexpr (kF32) {
-            nt_store16(o, __builtin_bit_cast(v4u, lo));
-            nt_store16(o + 16, __builtin_bit_cast(v4u, hi));
+            store16(o, __builtin_bit_cast(v4u, lo));
+            store16(o + 16, __builtin_bit_cast(v4u, hi));
           } else {
-            nt_store16(o, v4u{f32x2_to_bf16(lo[0], lo[1]), f32x2_to_bf16(lo[2], lo[3]), f32x2_to_bf16(hi[0], hi[1]),
-                              f32x2_to_bf16(hi[2], hi[3])});
+            store16(o, v4u{f32x2_to_bf16(lo[0], lo[1]), f32x2_to_bf16(lo[2], lo[3]), f32x2_to_bf16(hi[0], hi[1]),
+                           f32x2_to_bf16(hi[2], hi[3])});
           }
         }
     }

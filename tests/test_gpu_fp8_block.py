@@ -178,6 +178,96 @@ def test_grouped(flags, gather, name, K, N, dtype):
         within(y[at], want, err, f"expert {e}")
 
 
+def many_groups(seed, E=40, most=260):
+    """Ragged groups whose items are several to each workgroup: offsets, pairs (two a token), expert of each row."""
+    sizes = torch.randint(0, most, (E,), generator=torch.Generator().manual_seed(seed))
+    sizes[::7] = 0
+    P = (int(sizes.sum()) + 5) // 2 * 2
+    off = torch.cat([torch.tensor([2]), 2 + sizes.cumsum(0)]).int().cuda()
+    expert = torch.full((P,), -1)
+    expert[2:2 + int(sizes.sum())] = torch.repeat_interleave(torch.arange(E), sizes)
+    pair = torch.randperm(P, generator=torch.Generator().manual_seed(seed)).int().cuda()
+    return off, pair, expert.cuda(), P, E
+
+
+@pytest.mark.parametrize("dtype", [BF, FS])
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 1280])
+def test_grouped_items_that_run_on_into_the_next(dtype, K):
+    """Several items to a workgroup: loads of the next one under the last stages, no wait for the stores."""
+    N = 2080
+    off, pair, expert, P, E = many_groups(K)
+    g = gen(K)
+    xq, xs = make_rows(g, P // 2, K)
+    wq, ws = make_weights(g, E, N, K)
+    w, x = moe.fp8_block_prepack(wq, ws), ref.rows(xq, xs)
+    for gather in (False, True):
+        y = torch.full((P, N), 7.0, dtype=dtype, device="cuda")
+        if gather:
+            moe.fp8_block_grouped(w, xq, xs, off, rows=pair, row_div=2, flags=PRE, y=y)
+            r = (pair // 2).long()
+        else:  # the same rows in expert order
+            r = (pair // 2).long()
+            moe.fp8_block_grouped(w, xq[r].contiguous(), xs[:, r].contiguous(), off, flags=PRE, y=y)
+        assert (y[expert < 0] == 7).all()
+        for e in range(E):
+            at = expert == e
+            want, err = ref.product(x[r[at]], ref.weights(wq[e], ws[e]), ref.HALF[dtype])
+            within(y[at], want, err, f"expert {e}, gather {gather}")
+
+
+@pytest.mark.parametrize("K", [128, 256, 384, 1024])
+def test_gated_items_that_run_on_into_the_next(K):
+    N = 1024
+    off, pair, expert, P, E = many_groups(K + 1)
+    g = gen(K)
+    xq, xs = make_rows(g, P // 2, K)
+    (wq, ws), (uq, us) = make_weights(g, E, N, K), make_weights(g, E, N, K)
+    x, r = ref.rows(xq, xs), (pair // 2).long()
+    for save in (False, True):
+        q, s = torch.full((P, N), 9, dtype=torch.uint8, device="cuda"), torch.full((N // 128, P), 7.0, device="cuda")
+        _, _, gate, up = moe.fp8_block_glu(moe.fp8_block_prepack_glu(wq, ws, uq, us), xq, xs, off, rows=pair, row_div=2,
+                                           flags=PRE, q=q, s=s, save=save)
+        assert (q[expert < 0] == 9).all() and (s[:, expert < 0] == 7).all()
+        for e in range(E):
+            at = expert == e
+            if at.any():
+                (a, ea), (b, eb), (h, eh) = ref.glu(x[r[at]], ref.weights(wq[e], ws[e]), ref.weights(uq[e], us[e]))
+                within(ref.rows(q[at], s[:, at]), h, ref.held(h, eh), f"expert {e}")
+                if save:
+                    within(gate[at], a, ea + ref.HALF[BF] * (a.abs() + ea), "gate")
+                    within(up[at], b, eb + ref.HALF[BF] * (b.abs() + eb), "up")
+    wq, ws = make_weights(g, E, K, N)
+    gate, up = (2 * normal(g, P, N)).to(BF), normal(g, P, N).to(BF)
+    xq, xs = xq[r].contiguous(), xs[:, r].contiguous()
+    q, s = moe.fp8_block_glu_backward(moe.fp8_block_prepack_t(wq, ws), xq, xs, gate, up, off, flags=PRE)
+    for e in range(E):
+        at = expert == e
+        if at.any():
+            dh, adh = ref.product(ref.rows(xq, xs)[at], ref.weights(wq[e], ws[e]).T.contiguous())
+            (dg, ag), (du, au) = ref.glu_grad(dh, adh, gate[at].double(), up[at].double())
+            v = ref.rows(q[at], s[:, at])
+            within(v[:, :N], dg, ref.held(dg, ag), f"dg, expert {e}")
+            within(v[:, N:], du, ref.held(du, au), f"du, expert {e}")
+
+
+def test_rows_of_y_past_32_bits():
+    """Outputs of more than 2^32 elements: the first and the last rows."""
+    g = gen(21)
+    P, N = 270000, 16384
+    xq, xs = make_rows(g, 300, 128)
+    wq, ws = make_weights(g, 2, N, 128)
+    w = moe.fp8_block_prepack(wq, ws)
+    rows = (torch.arange(P, device="cuda", dtype=torch.int32) * 7) % 300
+    off = torch.tensor([0, P - 40, P], dtype=torch.int32, device="cuda")
+    x = ref.rows(xq, xs)[rows.long()]
+    for flags in (DEC, PRE):
+        y = moe.fp8_block_grouped(w, xq, xs, off, rows=rows, flags=flags)
+        for e, a, b in ((0, 0, 300), (0, P - 300, P - 40), (1, P - 40, P)):
+            want, err = ref.product(x[a:b], ref.weights(wq[e], ws[e]), ref.HALF[BF])
+            within(y[a:b], want, err, f"rows {a}")
+        del y
+
+
 def test_grouped_offsets_and_rows_out_of_range_stay_inside():
     g = gen(5)
     xq, xs = make_rows(g, 40, 256)
@@ -350,14 +440,14 @@ def test_weight_grad_nan_row_stays_in_its_group():
 
 
 # ------------------------------------------------------------- as it is used
-def feed_forward(w, x, do, off, pair, k, ws=None):
+def feed_forward(w, x, do, off, pair, k, flags=0):
     """One expert layer's forward and backward pass as a program makes them."""
     xq, xs = moe.quant_fp8_block(x)
-    hq, hs, gate, up = moe.fp8_block_glu(w["w13"], xq, xs, off, rows=pair, row_div=k, save=True)
-    o = moe.fp8_block_grouped(w["w2"], hq, hs, off)
+    hq, hs, gate, up = moe.fp8_block_glu(w["w13"], xq, xs, off, rows=pair, row_div=k, save=True, flags=flags)
+    o = moe.fp8_block_grouped(w["w2"], hq, hs, off, flags=flags)
     dq, ds = moe.quant_fp8_block(do)
-    gq, gs = moe.fp8_block_glu_backward(w["w2_t"], dq, ds, gate, up, off)
-    dx = moe.fp8_block_grouped(w["w13_t"], gq, gs, off, dtype=FS)
+    gq, gs = moe.fp8_block_glu_backward(w["w2_t"], dq, ds, gate, up, off, flags=flags)
+    dx = moe.fp8_block_grouped(w["w13_t"], gq, gs, off, dtype=FS, flags=flags)
     dw2 = moe.fp8_block_weight_grad(dq, ds, hq, hs, off)
     dw13 = moe.fp8_block_weight_grad(gq, gs, xq, xs, off, rows=pair, row_div=k)
     return o, dx, dw2, dw13
@@ -394,24 +484,25 @@ def test_forward_and_backward_chain(T):
         assert (a.double() - b).norm() < 0.1 * b.norm(), what
 
 
-def test_chain_in_a_graph_and_on_another_stream():
+@pytest.mark.parametrize("flags", [DEC, PRE])
+def test_chain_in_a_graph_and_on_another_stream(flags):
     w, m, x, do, off, pair, k, E = training_case()
-    want = feed_forward(w, x, do, off, pair, k)
+    want = feed_forward(w, x, do, off, pair, k, flags)
     stream = torch.cuda.Stream()
     stream.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(stream):
-        again = feed_forward(w, x, do, off, pair, k)
+        again = feed_forward(w, x, do, off, pair, k, flags)
     stream.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(again, want))
     graph = torch.cuda.CUDAGraph()
     xs, dos = x.clone(), do.clone()
     with torch.cuda.graph(graph):
-        out = feed_forward(w, xs, dos, off, pair, k)
+        out = feed_forward(w, xs, dos, off, pair, k, flags)
     for i in range(3):
         xs.copy_(x * (i + 1))
         dos.copy_(do * 0.5 ** i)
         graph.replay()
-        eager = feed_forward(w, xs, dos, off, pair, k)
+        eager = feed_forward(w, xs, dos, off, pair, k, flags)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, eager)), i
 
