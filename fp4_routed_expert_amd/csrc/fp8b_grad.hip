@@ -3,21 +3,25 @@
 //
 // The sum runs over rows, along which both scales vary, so the products are made
 // in the fp16 matrix cores (the rate of bf16, three bits more).  x's codes are
-// exact in fp16; dy's codes are multiplied by both scales, once for each of the
-// tile's two blocks of k.  The scales' products are divided first by a power of two
-// that brings the largest of the group's rows to [2^4, 2^6), so that the range of
-// fp16 costs nothing: a product's two roundings, of the scale and of the product, are
-// 2^-10 of it, and for rows whose scales are 2^-20 of the largest and less 2^-31 of
-// that.  The sums are fp32.
+// exact in fp16; dy's codes are multiplied by both scales.  The scales' products are
+// divided first by a power of two that brings that of the group's largest ones to
+// [2^4, 2^6), so that the range of fp16 costs little: a product's two roundings, of the
+// scale and of the product, are 2^-10 of it, and where the scales are less than 2^-18 of
+// the largest ones 2^-29 of what those would make.  The sums are fp32.
 //
 // A workgroup makes 256 x 256 outputs of one expert, eight waves of 64 x 128 by
 // v_mfma_f32_32x32x16_f16, in steps of 32 rows.  The matrix cores want eight
-// neighbouring rows of one column in a lane: a thread reads four bytes of eight
-// rows each, converts them to pairs of columns and swaps halves to pairs of rows.
-// Waves 0-3 convert dy, waves 4-7 x, each between its MFMAs; a SIMD has one of
-// either.  LDS holds [eight rows][column c of four][group of four columns], 16 bytes
-// each, so that writes and reads run along neighbouring addresses; a lane ends with
-// four neighbouring outputs.
+// neighbouring rows of one column in a lane.  The codes go to LDS by LDS-DMA as they
+// are, four steps of them; transposing LDS reads bring eight rows of a column to each
+// lane, which converts them itself.  (A column of dy is converted by two waves, one of
+// x by four.  Converted once, by one wave each, and handed on through LDS in fp16, the
+// LDS port was the limit: 16384 rows, 4096 x 7168, 923 us, now 797; four waves of 128 x
+// 128, which convert less but leave a SIMD with one wave, 860.)
+//
+// Bound by what two waves per SIMD issue (the matrix cores are busy 58 % of the time,
+// 66 % of the rounds that 448 tiles take on 256 CUs) and by the power limit: 1.85 GHz.
+// 16384 rows, 4096 x 7168: 1.2 PFLOP/s; 64 experts of 432 rows, 4096 x 1536: 437 us,
+// 0.8 PFLOP/s, where a tile's start and its stores count.
 //
 // Where the tiles are fewer than the CUs, the rows are split; the parts' sums go
 // through memory in fp32 and are added in the order of the rows.
@@ -32,16 +36,16 @@ namespace {
 
 constexpr int kTile = 256;
 constexpr int kStepRows = 32;
-constexpr int kPanel = kTile * kStepRows * 2;  // bytes of one operand's step in fp16
-constexpr int kBuf = 3 * kPanel;               // dy for each block of k, x
-constexpr int kCodes = kTile * kStepRows;      // bytes of one operand's step as codes
-constexpr int kRawSteps = 3;
-constexpr int kPanelTiles = 8;                 // k tiles of a panel of the walk
-// LDS: two steps in fp16, three steps of codes (dy, x), four of scales (dy's blocks 0
-// and 1, x's; 32 rows each, twice), two of their products, eight of row indices
-constexpr int kOffRaw = 2 * kBuf, kOffScale = kOffRaw + kRawSteps * 2 * kCodes, kOffProd = kOffScale + 4 * 1024;
-constexpr int kOffIdx = kOffProd + 2 * 256, kOffTop = kOffIdx + 8 * 256, kLds = kOffTop + 128;
-static_assert(kLds <= 160 * 1024, "LDS");
+constexpr int kCodes = kTile * kStepRows;  // bytes of one operand's step
+constexpr int kRing = 4;                   // steps in LDS
+constexpr int kPanelTiles = 8;             // k tiles of a panel of the walk
+// LDS: the steps' codes (dy, x), their scales (dy's blocks 0 and 1, x's; 32 rows each,
+// twice), two steps' products of them, row indices of twice as many steps
+constexpr int kOffScale = kRing * 2 * kCodes, kOffProd = kOffScale + kRing * 1024;
+constexpr int kOffIdx = kOffProd + 2 * 256, kOffTop = kOffIdx + 2 * kRing * 256;
+constexpr int kOut = 16 * 1024;  // of a wave, at the end: 64 rows of 128 outputs in bf16, or 32 in fp32
+constexpr int kLds = 8 * kOut;
+static_assert(kOffTop + 128 <= kLds && kLds <= 160 * 1024, "LDS");
 
 struct GradLaunch {
   Fp8bGradArgs a;
@@ -53,12 +57,29 @@ struct GradLaunch {
 
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef int v2i __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ v16f mfma_f16(v4u a, v4u b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 __device__ __forceinline__ uint32_t mul_pair(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, a) * __builtin_bit_cast(v2h, b));
+}
+
+// Each lane of 16 gives the address of eight neighbouring bytes, the lanes 2 i and 2 i
+// + 1 those of row i, and gets its column's byte of the eight rows.
+__device__ __forceinline__ v2i lds_columns(uint32_t addr) {
+  return __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<__attribute__((address_space(3))) v2i*>((uintptr_t)addr));
+}
+// Eight codes as fp16.
+__device__ __forceinline__ v4u to_half(v2i c) {
+  v4u w;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i], 1.0f, false));
+    w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i], 1.0f, true));
+  }
+  return w;
 }
 
 // x row of each row of dy
@@ -106,181 +127,162 @@ struct GradCtx {
   int up_y, up_x;         // powers of two for a dy wave's products
 };
 
-// The loop of a wave that moves and converts x (kIsX) or dy: rows 8 o .. 8 o + 7 of
-// a step, by LDS-DMA as they are, then four columns a thread.
+// The loop of a wave; it moves rows 8 o .. 8 o + 7 of every step of x (kIsX) or dy.
 template <bool kIsX, bool kGather>
-__device__ __forceinline__ void run_rows(const GradCtx& g, v16f (&acc)[2][4]) {
+__device__ __forceinline__ void run_rows(const GradCtx& g, v16f (&acc)[4][2]) {
   const uint32_t lds0 = g.lds0;
   const int lane = g.lane, wave = g.wave, begin = g.begin, steps = g.steps, width = g.width;
-  // products: n rows 4 q + c for q of half wn % 2 (block wn % 2), c = 2 (wn / 2) + {0, 1}; k columns of block wk
-  const int wn = wave >> 1, wk = wave & 1, r = lane & 31, h = lane >> 5;
+  const int wn = wave >> 1, wk = wave & 1, h = lane >> 5;
   const int o = wave & 3;
-  // (columns past the last one read the last 16: not stored)
-  const uint32_t piece = (uint32_t)min(kTile * g.tile + 16 * (lane & 15), width - 16);
   const uint8_t* base = g.codes;
   const uint32_t last = (uint32_t)(g.end - 1);
   auto row_at = [&](int step, int r) { return min((uint32_t)begin + (uint32_t)(kStepRows * step + r), last); };
   auto entry = [&](int step, int r) {  // of the index ring
-    return (uint32_t)lds_i32(lds0 + kOffIdx + 256u * (uint32_t)(step & 7) + 4u * (uint32_t)r);
+    return (uint32_t)lds_i32(lds0 + kOffIdx + 256u * (uint32_t)(step & (2 * kRing - 1)) + 4u * (uint32_t)r);
   };
-  auto load_codes = [&](int step, int slot) {
-    const uint32_t to = lds0 + (uint32_t)(kOffRaw + (2 * slot + (kIsX ? 1 : 0)) * kCodes + 2048 * o);
+  // A row's piece p of 16 bytes lies at p ^ 2 (row % 8), so that eight rows' pieces of
+  // neighbouring columns are in different banks.  (Columns past the last one read the
+  // last 16: not stored.)
+  uint32_t piece[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int r = 8 * o + 4 * t + (lane >> 4);
-      if constexpr (kIsX && kGather) {
-        dma16_lanes(base + (size_t)entry(step, r) * (size_t)width + piece, to + 1024u * t);
-      } else {
-        const uint32_t first = wave_u32(row_at(step, 0));
-        dma16(base + (size_t)first * (size_t)width, (row_at(step, r) - first) * (uint32_t)width + piece, to + 1024u * t);
-      }
-    }
+  for (int t = 0; t < 2; ++t)
+    piece[t] = (uint32_t)min(kTile * g.tile + 16 * ((lane & 15) ^ (2 * (4 * t + (lane >> 4)))), width - 16);
+  // Loads of a step: codes, scales (dy wave o those of dy's block o, or of x's block o -
+  // 2) and, much further ahead, row indices.  A lane's offsets from the step's first
+  // row change only where the rows end.
+  uint32_t code_off[2], scale_off, entry_off;
+  auto first_of = [&](int step) { return wave_u32(min((uint32_t)begin + (uint32_t)(kStepRows * step), last)); };
+  auto word_of = [&](int step) { return 4u * min((uint32_t)(lane & 31), last - first_of(step)); };
+  auto set_offsets = [&](int codes, int scales, int entries) {  // of these steps
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      code_off[t] = min((uint32_t)(8 * o + 4 * t + (lane >> 4)), last - first_of(codes)) * (uint32_t)width + piece[t];
+    scale_off = word_of(scales);
+    entry_off = word_of(entries);
   };
-  // scales: dy wave o those of dy's block o, or of x's block o - 2
-  auto load_scales = [&](int step) {
+  auto load_codes = [&](int step, int slot, int t) {
+    const uint32_t to = lds0 + (uint32_t)((2 * slot + (kIsX ? 1 : 0)) * kCodes + 2048 * o + 1024 * t);
+    if constexpr (kIsX && kGather)
+      dma16_lanes(base + (size_t)entry(step, 8 * o + 4 * t + (lane >> 4)) * (size_t)width + piece[t], to);
+    else
+      dma16(base + (size_t)first_of(step) * (size_t)width, code_off[t], to);
+  };
+  auto load_scales = [&](int step, int slot) {
     if constexpr (!kIsX) {
-      uint32_t r = row_at(step, lane & 31);
-      if (kGather && o >= 2) r = entry(step, lane & 31);
-      dma4_from(reinterpret_cast<const uint8_t*>(g.scales + r), lds0 + (uint32_t)(kOffScale + 1024 * (step & 3) + 256 * o));
+      const uint32_t to = lds0 + (uint32_t)(kOffScale + 1024 * slot + 256 * o);
+      if (kGather && o >= 2)
+        dma4_from(reinterpret_cast<const uint8_t*>(g.scales + entry(step, lane & 31)), to);
+      else
+        dma4(reinterpret_cast<const uint8_t*>(g.scales + first_of(step)), scale_off, to);
     }
   };
   auto load_entries = [&](int step) {
     if constexpr (kIsX && kGather)
-      dma4_from(reinterpret_cast<const uint8_t*>(g.xrows + row_at(step, lane & 31)),
-                lds0 + (uint32_t)(kOffIdx + 256 * (step & 7)));
+      dma4(reinterpret_cast<const uint8_t*>(g.xrows + first_of(step)), entry_off,
+           lds0 + (uint32_t)(kOffIdx + 256 * (step & (2 * kRing - 1))));
   };
   constexpr int kLoads = kIsX ? (kGather ? 3 : 2) : 3;  // of a step
-  auto load = [&](int j, int slot) {  // behind step j's barrier
-    load_codes(j + 4, slot);
-    load_scales(j + 5);
-    load_entries(j + 8);
-  };
   // products of the scales, one of the four pairs of blocks a dy wave, for 32 rows (the upper lanes repeat them)
-  const int sn = o >> 1, sk = o & 1;
   float fy, fx;
-  auto get_scales = [&](int step) {
+  const uint32_t scales_at = lds0 + (uint32_t)(kOffScale + 256 * (o >> 1) + 4 * (lane & 31));
+  const uint32_t x_scales_at = lds0 + (uint32_t)(kOffScale + 512 + 256 * (o & 1) + 4 * (lane & 31));
+  const uint32_t product_at = lds0 + (uint32_t)(kOffProd + 64 * o + 2 * (lane & 31));
+  auto get_scales = [&](int slot) {
     if constexpr (!kIsX) {
-      const uint32_t at = lds0 + (uint32_t)(kOffScale + 1024 * (step & 3)) + 4u * (uint32_t)(lane & 31);
-      fy = __int_as_float(lds_i32(at + 256u * sn));
-      fx = __int_as_float(lds_i32(at + 512u + 256u * sk));
+      fy = __int_as_float(lds_i32(scales_at + 1024u * slot));
+      fx = __int_as_float(lds_i32(x_scales_at + 1024u * slot));
     }
   };
-  auto put_products = [&](int step) {
+  auto put_products = [&](int step, int slot) {
     if constexpr (!kIsX) {
-      const float k = __builtin_amdgcn_ldexpf(fy, g.up_y) * __builtin_amdgcn_ldexpf(fx, g.up_x);
-      const bool live = (uint32_t)begin + (uint32_t)(kStepRows * step + (lane & 31)) <= last;
-      *reinterpret_cast<__attribute__((address_space(3))) _Float16*>((uintptr_t)(
-          lds0 + (uint32_t)(kOffProd + 256 * (step & 1) + 64 * (2 * sn + sk) + 2 * (lane & 31)))) = (_Float16)(live ? k : 0.0f);
+      float k = __builtin_amdgcn_ldexpf(fy, g.up_y) * __builtin_amdgcn_ldexpf(fx, g.up_x);
+      if (step >= steps - 1)  // rows past the last one
+        k = (uint32_t)begin + (uint32_t)(kStepRows * step + (lane & 31)) <= last ? k : 0.0f;
+      *reinterpret_cast<__attribute__((address_space(3))) _Float16*>((uintptr_t)(product_at + 256u * (slot & 1))) = (_Float16)k;
     }
   };
-  // a step's conversion in pieces: its codes; two rows to fp16; the scales' products; each column
-  uint32_t raw[8], v[8][2], k[2][4];
-  auto get_codes = [&](int slot) {
-    const uint32_t at = lds0 + (uint32_t)(kOffRaw + (2 * slot + (kIsX ? 1 : 0)) * kCodes + 2048 * o) + 4u * (uint32_t)lane;
+  // A wave's 64 columns of dy (f = 4, 5) and 128 of x (f < 4), for 16 rows u of a step:
+  // lane l holds eight rows 8 (l / 32) of column l % 32 of 32.
+  v2i raw[6];
+  v4u half[2][6], k;
+  uint32_t at[6];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = (uint32_t)lds_i32(at + 256u * i);
-  };
-  auto rows_to_half = [&](int m) {
-#pragma unroll
-    for (int i = 2 * m; i < 2 * m + 2; ++i) {
-      v[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)raw[i], 1.0f, false));
-      v[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)raw[i], 1.0f, true));
-    }
-  };
-  auto get_products = [&](int step) {
-    if constexpr (!kIsX) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const v4u t = lds_v4(lds0 + (uint32_t)(kOffProd + 256 * (step & 1) + 64 * b + 16 * o) + 128u * (uint32_t)(lane >> 5));
-        k[b][0] = t.x, k[b][1] = t.y, k[b][2] = t.z, k[b][3] = t.w;
-      }
-    }
-  };
-  const uint32_t my_column = lds0 + (uint32_t)((kIsX ? 2 * kPanel : 0) + o * kTile * 16) + 16u * (uint32_t)lane;
-  auto put_column = [&](int step, int c) {
-    lds_words* to = reinterpret_cast<lds_words*>((uintptr_t)(my_column + (uint32_t)((step & 1) * kBuf + 1024 * c)));
-    v4u w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)  // halves c % 2 of rows 2 i and 2 i + 1
-      w[i] = __builtin_amdgcn_perm(v[2 * i + 1][c >> 1], v[2 * i][c >> 1], c & 1 ? 0x07060302u : 0x05040100u);
-    if constexpr (kIsX) {
-      *to = w;
-    } else {
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        to[b * (kPanel / 16)] =
-            v4u{mul_pair(w[0], k[b][0]), mul_pair(w[1], k[b][1]), mul_pair(w[2], k[b][2]), mul_pair(w[3], k[b][3])};
-    }
-  };
-  // fragments of 16 rows u of a step
-  v4u fa[2], fb[4];
-  const uint32_t pa = lds0 + (uint32_t)(wk * kPanel) + 16u * (uint32_t)(h * kTile + 128 * (wn >> 1) + 32 * (wn & 1) + r);
-  const uint32_t pb = lds0 + (uint32_t)(2 * kPanel) + 16u * (uint32_t)(h * kTile + 32 * wk + r);
-  auto read_a = [&](int step, int u, int i) { fa[i] = lds_v4(pa + (uint32_t)((step & 1) * kBuf + (2 * u * kTile + 64 * i) * 16)); };
-  auto read_b = [&](int step, int u, int c) { fb[c] = lds_v4(pb + (uint32_t)((step & 1) * kBuf + (2 * u * kTile + 64 * c) * 16)); };
-  // Step j: its products, while step j + 1 is converted and the scales' products of
-  // step j + 2 are made.  Behind three quarters of the MFMAs a barrier publishes
-  // these, and the codes of step j + 2, which have had two steps to arrive; their
-  // place takes those of step j + 4, and the next step's fragments are read under
-  // the last MFMAs.  (Loads past the last step read its rows again; a step past the
-  // last has products of zero.)
-  auto iterate = [&](int j, int slot) __attribute__((always_inline)) {  // slot: (j + 1) % 3
-    each([&](auto at) __attribute__((always_inline)) {
-      constexpr int m = decltype(at)::value, u = m >> 3, i = (m >> 2) & 1, c = m & 3;
-      acc[i][c] = mfma_f16(fa[i], fb[c], acc[i][c]);
-      if (m == 0) {
-        get_codes(slot);
-        get_products(j + 1);
-        get_scales(j + 2);
-      }
-      // the second 16 rows' fragments, each behind its register's last use
-      if (u == 0 && c == 3) read_a(j, 1, i);
-      if (u == 0 && i == 1) read_b(j, 1, c);
-      if (m >= 2 && m < 6) rows_to_half(m - 2);
-      if (m >= 6 && m < 10) put_column(j + 1, m - 6);
-      if (m == 10) put_products(j + 2);
-      if (m == 12) {
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
-        load(j, slot);
-        read_a(j + 1, 0, 0);
-      }
-      if (u == 1 && i == 1) read_b(j + 1, 0, c);
-      if (m == 15) read_a(j + 1, 0, 1);
-      if (c == 3) __builtin_amdgcn_sched_barrier(0);  // (four MFMAs at a time are the compiler's to order)
-    }, std::make_integer_sequence<int, 16>{});
+  for (int f = 0; f < 6; ++f) {
+    const int p = (f < 4 ? 8 * wk + 2 * f : 4 * wn + 2 * (f - 4)) + ((lane >> 4) & 1), r = (lane & 15) >> 1;
+    at[f] = opaque(lds0 + (uint32_t)((f < 4 ? kCodes : 0) + 256 * (8 * h + r) + 16 * (p ^ (2 * r)) + 8 * (lane & 1)));
+  }
+  const uint32_t my_products = opaque(lds0 + (uint32_t)(kOffProd + 64 * (2 * (wn >> 1) + wk) + 16 * h));
+  auto get_codes = [&](int slot, int u, int f) { raw[f] = lds_columns(at[f] + (uint32_t)(slot * 2 * kCodes + 4096 * u)); };
+  auto get_products = [&](int slot, int u) { k = lds_v4(my_products + (uint32_t)(256 * (slot & 1) + 32 * u)); };
+  auto convert = [&](int u, int f) __attribute__((always_inline)) {
+    v4u w = to_half(raw[f]);
+    if (f >= 4) w = v4u{mul_pair(w[0], k[0]), mul_pair(w[1], k[1]), mul_pair(w[2], k[2]), mul_pair(w[3], k[3])};
+    half[u][f] = w;
   };
   // the first steps' codes, scales and (by plain loads) indices
-  if constexpr (kIsX && kGather) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      *reinterpret_cast<__attribute__((address_space(3))) int*>((uintptr_t)(lds0 + (uint32_t)(kOffIdx + 256 * q) + 4u * (uint32_t)lane)) =
-          g.xrows[row_at(q, lane & 31)];
-  }
+  if constexpr (kGather)
+    *reinterpret_cast<__attribute__((address_space(3))) int*>((uintptr_t)(lds0 + (uint32_t)(kOffIdx + 256 * wave) + 4u * (uint32_t)lane)) =
+        g.xrows[row_at(wave, lane & 31)];
   __syncthreads();
-#pragma unroll
-  for (int q = 0; q < 3; ++q) load_codes(q, q);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) load_scales(q);
+  each([&](auto q_) {
+    constexpr int q = decltype(q_)::value;
+    set_offsets(q, q, q);
+    load_codes(q, q, 0);
+    load_codes(q, q, 1);
+    load_scales(q, q);
+  }, std::make_integer_sequence<int, kRing>{});
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     get_scales(q);
-    put_products(q);
+    put_products(q, q);
   }
-  get_codes(0);
   __syncthreads();
-  get_products(0);
+  set_offsets(kRing, kRing, kRing);
+  load_scales(kRing, 0);
+  get_products(0, 0);
 #pragma unroll
-  for (int m = 0; m < 4; ++m) rows_to_half(m);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) put_column(0, c);
-  __syncthreads();
-  load(-1, 0);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) read_a(0, 0, i);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) read_b(0, 0, c);
-  for (int j = 0, slot = 1; j < steps; ++j, slot = slot == 2 ? 0 : slot + 1) iterate(j, slot);
+  for (int f = 0; f < 6; ++f) {
+    get_codes(0, 0, f);
+    convert(0, f);
+    get_codes(0, 1, f);
+  }
+  get_products(0, 1);
+  // Step j, in place j % kRing: under the products of 16 rows the next 16 rows' codes
+  // are converted, and those behind them read.  The barrier publishes step j + 1, its
+  // scales' products and the scales of step j + 2, and frees step j's place, whose
+  // codes are in registers.  (Loads past the last step read its last row again; a step
+  // past the last has products of zero.)  What a wave issues counts: an instruction
+  // takes it eight clocks, an MFMA 32, and a SIMD has two waves, so that the places are
+  // constants and the loads' offsets are kept (836 us without, now 797).
+  int j = 0;
+  auto step = [&](auto place) __attribute__((always_inline)) {
+    constexpr int p = decltype(place)::value, next = (p + 1) % kRing, after = (p + 2) % kRing;
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kRing - 2) * kLoads) : "memory");
+    if (j + (kGather ? 2 * kRing : kRing + 1) >= steps - 1)  // the rows end in these loads
+      set_offsets(j + kRing, j + kRing + 1, j + 2 * kRing);
+    each([&](auto m_) __attribute__((always_inline)) {
+      constexpr int m = decltype(m_)::value, u = m >> 3, q = m & 7, c = q >> 1, i = q & 1;
+      acc[c][i] = mfma_f16(half[u][c], half[u][4 + i], acc[c][i]);
+      if constexpr (q < 6) {
+        convert(u ^ 1, q);
+        get_codes(next, u, q);
+      }
+      if (q == 6) get_products(next, u);
+      if (m == 0) get_scales(after);
+      if (m == 6) load_codes(j + kRing, p, 0);
+      if (m == 7) load_codes(j + kRing, p, 1);
+      if (m == 14) load_scales(j + kRing + 1, next);
+      if (m == 15) load_entries(j + 2 * kRing);
+      if (m == 10) put_products(j + 2, after);
+      if (i == 1) __builtin_amdgcn_sched_barrier(0);
+    }, std::make_integer_sequence<int, 16>{});
+    return ++j < steps;
+  };
+  static_assert(kRing == 4, "places of the loop");
+  while (step(std::integral_constant<int, 0>{}) && step(std::integral_constant<int, 1>{}) &&
+         step(std::integral_constant<int, 2>{}) && step(std::integral_constant<int, 3>{})) {
+  }
   wait_vmcnt<0>();  // the loads past the last step land before the LDS is given back
 }
 
@@ -320,10 +322,13 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const float* p[4] = {a.ys + (size_t)nb0 * a.P, a.ys + (size_t)nb1 * a.P, a.xs + (size_t)kb0 * a.X,
                          a.xs + (size_t)kb1 * a.X};
     float top[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = begin + tid; s < end; s += 512) {
-      const int x = x_row(s);
+    for (long first = begin + tid; first < end; first += 4 * 512) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], fabsf(p[i][i < 2 ? s : x]));
+      for (int u = 0; u < 4; ++u) {
+        const int s = (int)min(first + 512 * u, (long)end - 1), x = x_row(s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], fabsf(p[i][i < 2 ? s : x]));
+      }
     }
     float(*tops)[4] = reinterpret_cast<float(*)[4]>(lds + kOffTop);
 #pragma unroll
@@ -343,13 +348,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
   constexpr int kUp = 6;  // the scales' products are brought below 2^kUp, times 448 below 2^15
 
-  // products: n rows 4 q + c for q of half wn % 2 (block wn % 2), c = 2 (wn / 2) + {0, 1}; k columns of block wk
-  const int wn = wave >> 1, wk = wave & 1, r = lane & 31, h = lane >> 5;
-  v16f acc[2][4];
+  const int wn = wave >> 1, wk = wave & 1;  // columns 64 wn of dy, 128 wk of x
+  v16f acc[4][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
@@ -368,29 +372,62 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       run_rows<false, kGather>(c, acc);
     }
   }
-  const int down = (wn & 1 ? y_exp[1] : y_exp[0]) + (wk ? x_exp[1] : x_exp[0]) - kUp;
+  const int down = (wn >> 1 ? y_exp[1] : y_exp[0]) + (wk ? x_exp[1] : x_exp[0]) - kUp;
 
-  // element v of a lane: row q = 32 (wn % 2) + 8 (v / 4) + 4 h + v % 4, its four columns in the four tiles
-  const int k0 = kTile * tk + 128 * wk + 4 * r;
-  if (k0 >= a.K) return;
-  const size_t plane = (size_t)a.N * a.K;
-  float* sums = g.parts > 1 ? g.partial + ((size_t)part * a.E + e) * plane : static_cast<float*>(a.dw) + (size_t)e * plane;
-  uint16_t* half = static_cast<uint16_t*>(a.dw) + (size_t)e * plane;
+  // Element v of a lane: column n = lane % 32 of dy, column 8 (v / 4) + 4 (lane / 32) +
+  // v % 4 of x.  They go through LDS (piece q of 16 bytes of row n at q ^ n), so that
+  // whole rows of the wave's 128 columns are stored, past the caches: 64 experts of
+  // 432 rows, 4096 x 1536, 447 us; 474 with cached stores, 530 with stores of 32 bytes of
+  // a row at a time from the registers.
+  __syncthreads();  // nobody reads codes any more
+  const int n0 = kTile * tn + 64 * wn, k0 = kTile * tk + 128 * wk, h = lane >> 5, n = lane & 31;
+  if (n0 >= a.N || k0 >= a.K) return;
+  const size_t plane = (size_t)a.N * a.K, first = (size_t)n0 * a.K + k0;
+  const uint32_t mine = lds0 + (uint32_t)(wave * kOut);
+  auto words = [&](int row, int bytes, int q) {
+    return reinterpret_cast<lds_words*>((uintptr_t)(mine + (uint32_t)(row * bytes) + 16u * (uint32_t)(q ^ (row & (bytes / 16 - 1)))));
+  };
+  if (kF32 || g.parts > 1) {
+    float* out = (g.parts > 1 ? g.partial + ((size_t)part * a.E + e) * plane : static_cast<float*>(a.dw) + (size_t)e * plane) + first;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int n = kTile * tn + 4 * (32 * (wn & 1) + 8 * (v >> 2) + 4 * h + (v & 3)) + 2 * (wn >> 1) + i;
-      if (n >= a.N) continue;
-      const size_t at = (size_t)n * a.K + k0;
-      const v4f s = {__builtin_amdgcn_ldexpf(acc[i][0][v], down), __builtin_amdgcn_ldexpf(acc[i][1][v], down),
-                     __builtin_amdgcn_ldexpf(acc[i][2][v], down), __builtin_amdgcn_ldexpf(acc[i][3][v], down)};
-      if (kF32 || g.parts > 1)
-        __builtin_nontemporal_store(s, reinterpret_cast<global<v4f>*>((uintptr_t)(sums + at)));
-      else
-        __builtin_nontemporal_store(v2u{f32x2_to_bf16(s[0], s[1]), f32x2_to_bf16(s[2], s[3])},
-                                    reinterpret_cast<global<v2u>*>((uintptr_t)(half + at)));
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v4f s;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) s[v] = __builtin_amdgcn_ldexpf(acc[c][i][4 * j + v], down);
+          *words(n, 512, 8 * c + 2 * j + h) = __builtin_bit_cast(v4u, s);
+        }
+#pragma unroll
+      for (int t = 0; t < 16; ++t)
+        __builtin_nontemporal_store((v4u)*words(2 * t + h, 512, n), reinterpret_cast<global<v4u>*>((uintptr_t)(out + (size_t)(32 * i + 2 * t + h) * a.K + 4 * n)));
     }
+  } else {
+    uint16_t* out = static_cast<uint16_t*>(a.dw) + (size_t)e * plane + first;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t s[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            s[v] = f32x2_to_bf16(__builtin_amdgcn_ldexpf(acc[c][i][8 * w + 2 * v], down),
+                                 __builtin_amdgcn_ldexpf(acc[c][i][8 * w + 2 * v + 1], down));
+          // lanes of the lower half get columns 0-7 of 16, those of the upper one 8-15
+          const auto lo = __builtin_amdgcn_permlane32_swap(s[0], s[2], false, false);
+          const auto hi = __builtin_amdgcn_permlane32_swap(s[1], s[3], false, false);
+          *words(32 * i + n, 256, 4 * c + 2 * w + h) = v4u{lo[0], hi[0], lo[1], hi[1]};
+        }
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      const int row = 4 * t + (lane >> 4);
+      __builtin_nontemporal_store((v4u)*words(row, 256, lane & 15), reinterpret_cast<global<v4u>*>((uintptr_t)(out + (size_t)row * a.K + 8 * (lane & 15))));
+    }
+  }
 }
 
 // The parts' sums, in the order of the rows.

@@ -100,6 +100,28 @@ def test_dense(flags, dtype, T, K, N):
 
 
 @pytest.mark.parametrize("flags", [DEC, PRE])
+@pytest.mark.parametrize("dtype", [BF, FS])
+def test_dense_all_codes(flags, dtype):
+    """Every code.  In fp32 the products are exact; in bf16 eight neighbouring ones are added with 14 bits below the
+    largest, each off by less than 2^-13 of the largest one then."""
+    g = gen(41)
+    T, N, K = 70, 160, 512
+    xq = torch.randint(0, 256, (T, K), generator=g, device="cuda", dtype=torch.uint8)
+    wq = torch.randint(0, 256, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+    xq[(xq & 127) == 127] = 0x80
+    wq[(wq & 127) == 127] = 0x7E
+    xs, ws = torch.rand(K // 128, T, generator=g, device="cuda") + 0.1, torch.rand(2, K // 128, generator=g, device="cuda") - 0.5
+    y = moe.fp8_block_dense(moe.fp8_block_prepack(wq, ws), xq, xs, dtype=dtype, flags=flags)
+    x, w = ref.rows(xq, xs), ref.weights(wq, ws)
+    want, err = ref.product(x, w, ref.HALF[dtype])
+    if dtype == BF:
+        for k in range(0, K, 8):
+            top = (x[:, None, k:k + 8] * w[None, :, k:k + 8]).abs().amax(-1)
+            err = err + 8 * 2.0 ** -13 * (1 + ref.HALF[BF]) * top
+    within(y, want, err)
+
+
+@pytest.mark.parametrize("flags", [DEC, PRE])
 def test_dense_nan_stays_in_its_row(flags):
     g = gen(3)
     x = normal(g, 20, 256).to(BF)
@@ -387,12 +409,24 @@ def test_glu_grad_against_differences():
 
 
 def grad_bound(y, x, half):
-    """dw, and its largest error: dy times both scales is rounded to bf16 once (half a step of a value in [1, 2) is
-    2^-8: eight significant bits), behind two fp32 roundings; the sum of n products in fp32."""
+    """dw, and its largest error.  The scales' product is rounded to fp16 (2^-11 of it), dy's code times that again
+    (2^-11; together below 2^-10 (1 + 2^-11)), behind two fp32 roundings.  Below fp16's normal numbers, 2^-14, where the
+    first of them rounds to 2^-25: the largest product of scales is at least 2^4 there (its two factors lie in [1/2, 1)
+    2^6 together), so that this is 2^-29 of the largest row's scales, times 448 squared at most; a row's own product then
+    rounds to 2^-25 too, times a code of x of 448.  The sum of n products in fp32."""
     n = y.shape[0]
     want, mags = y.T.contiguous() @ x, y.abs().T.contiguous() @ x.abs()
-    a = (ref.HALF[BF] * (1 + 2.0 ** -22) + ref.gamma(n)) * mags
+    a = (2.0 ** -10 * (1 + 2.0 ** -10) + ref.gamma(n)) * mags
     return want, a + half * (want.abs() + a)
+
+
+def grad_floor(ys, xs, n):
+    """What the range of fp16 may cost n rows' sums: n (2^-29 448 448 + 2^-29 448) times the largest scales of the
+    blocks, [N, K] (both largest ones, of any rows: at least the largest product)."""
+    if n == 0:
+        return 0.0
+    top = ys.abs().double().amax(1).repeat_interleave(128).unsqueeze(1) * xs.abs().double().amax(1).repeat_interleave(128)
+    return n * 2.0 ** -29 * (448 * 448 + 448) * top
 
 
 @pytest.mark.parametrize("dtype", [BF, FS])
@@ -412,7 +446,7 @@ def test_weight_grad(dtype, gather, name, N, K):
     for e in range(E):
         at = expert == e
         want, err = grad_bound(y[at], x[at], ref.HALF[dtype])
-        within(dw[e], want, err + 1e-300, f"expert {e}")
+        within(dw[e], want, err + grad_floor(ys, xs, int(at.sum())) + 1e-300, f"expert {e}")
 
 
 @pytest.mark.parametrize("T", [0, 1, 33, 700, 2100])
@@ -425,8 +459,41 @@ def test_weight_grad_of_one_group(T, dtype):
     dw = moe.fp8_block_weight_grad(yq, ys, xq, xs, dtype=dtype)
     want, err = grad_bound(ref.rows(yq, ys), ref.rows(xq, xs), ref.HALF[dtype])
     assert dw.shape == (256, 128)
-    within(dw, want, err + 1e-300)
+    within(dw, want, err + grad_floor(ys, xs, T) + 1e-300)
     assert torch.equal(dw, moe.fp8_block_weight_grad(yq, ys, xq, xs, dtype=dtype))
+
+
+@pytest.mark.parametrize("parts", [False, True])
+def test_weight_grad_scales_of_all_sizes(parts):
+    """Rows whose scales lie up to 2^-60 apart, and the range of fp32 itself."""
+    g = gen(31)
+    P, N, K = (3000, 128, 256) if parts else (400, 256, 384)
+    (yq, ys), (xq, xs) = make_rows(g, P, N), make_rows(g, P, K)
+    for low, high in ((-30, 0), (-8, 0), (0, 40), (-100, -90)):
+        y2 = ys * torch.exp2(torch.randint(low, high, ys.shape, generator=g, device="cuda").float())
+        x2 = xs * torch.exp2(torch.randint(-20, 20, xs.shape, generator=g, device="cuda").float())
+        dw = moe.fp8_block_weight_grad(yq, y2, xq, x2, dtype=FS)
+        want, err = grad_bound(ref.rows(yq, y2), ref.rows(xq, x2), ref.HALF[FS])
+        within(dw, want, err + grad_floor(y2, x2, P) + 2.0 ** -149, f"{low} {high}")
+
+
+def test_weight_grad_all_codes():
+    """Every code of e4m3, and the not-a-numbers where they belong: a row of dw and a column of it."""
+    g = gen(32)
+    P, N, K = 130, 256, 128
+    yq = torch.randint(0, 256, (P, N), generator=g, device="cuda", dtype=torch.uint8)
+    xq = torch.randint(0, 256, (P, K), generator=g, device="cuda", dtype=torch.uint8)
+    yq[(yq & 127) == 127] = 1
+    xq[(xq & 127) == 127] = 0x81
+    ys, xs = torch.rand(N // 128, P, generator=g, device="cuda") + 0.5, torch.rand(K // 128, P, generator=g, device="cuda")
+    want, err = grad_bound(ref.rows(yq, ys), ref.rows(xq, xs), ref.HALF[BF])
+    within(moe.fp8_block_weight_grad(yq, ys, xq, xs), want, err + grad_floor(ys, xs, P))
+    yq[7, 33], xq[129, 100] = 0x7F, 0xFF
+    dw = moe.fp8_block_weight_grad(yq, ys, xq, xs)
+    bad = torch.zeros(N, K, dtype=torch.bool, device="cuda")
+    bad[33], bad[:, 100] = True, True
+    assert torch.equal(dw.isnan(), bad)
+    within(dw[~bad], want[~bad], (err + grad_floor(ys, xs, P))[~bad])
 
 
 def test_weight_grad_nan_row_stays_in_its_group():
