@@ -290,6 +290,43 @@ def test_rows_of_y_past_32_bits():
         del y
 
 
+@pytest.mark.parametrize("flags", [DEC, PRE])
+def test_codes_up_to_the_limit_of_32_bits(flags):
+    """The last rows of as many as a call takes (T K = 2^32 - 16384), and one more refused."""
+    g = gen(22)
+    T, K, N = 2 ** 18 - 1, 16384, 32
+    xq = torch.zeros(T, K, dtype=torch.uint8, device="cuda")
+    xs = torch.ones(K // 128, T, device="cuda")
+    at = torch.tensor([0, T // 2, T - 257, T - 2, T - 1], device="cuda")
+    xq[at], s = make_rows(g, 5, K)
+    xs[:, at] = s
+    wq, ws = make_weights(g, 1, N, K)
+    w = moe.fp8_block_prepack(wq, ws)
+    y = moe.fp8_block_dense(w, xq, xs, flags=flags)
+    want, err = ref.product(ref.rows(xq[at], s), ref.weights(wq[0], ws[0]), ref.HALF[BF])
+    within(y[at], want, err)
+    assert int((y != 0).any(1).sum()) == 5
+    with pytest.raises(moe.MoeError):
+        moe.fp8_block_dense(w, torch.cat([xq, xq[:1]]), torch.ones(K // 128, T + 1, device="cuda"), flags=flags)
+
+
+def test_weight_grad_rows_past_32_bits():
+    """Codes of more than 2^32 bytes: the last group's rows."""
+    g = gen(23)
+    P, N, K = 300000, 16384, 128
+    yq = torch.zeros(P, N, dtype=torch.uint8, device="cuda")
+    ys, xs = torch.ones(N // 128, P, device="cuda"), torch.ones(1, P, device="cuda")
+    xq = torch.zeros(P, K, dtype=torch.uint8, device="cuda")
+    yq[P - 50:], ys[:, P - 50:] = make_rows(g, 50, N)
+    xq[P - 50:], xs[:, P - 50:] = make_rows(g, 50, K)
+    off = torch.tensor([0, P - 50, P], dtype=torch.int32, device="cuda")
+    dw = moe.fp8_block_weight_grad(yq, ys, xq, xs, off)
+    s = ys[:, P - 50:].contiguous(), xs[:, P - 50:].contiguous()
+    want, err = grad_bound(ref.rows(yq[P - 50:], s[0]), ref.rows(xq[P - 50:], s[1]), ref.HALF[BF])
+    assert (dw[0] == 0).all()
+    within(dw[1], want, err + grad_floor(*s, 50))
+
+
 def test_grouped_offsets_and_rows_out_of_range_stay_inside():
     g = gen(5)
     xq, xs = make_rows(g, 40, 256)
@@ -572,6 +609,39 @@ def test_chain_in_a_graph_and_on_another_stream(flags):
         eager = feed_forward(w, xs, dos, off, pair, k, flags)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, eager)), i
+
+
+@pytest.mark.parametrize("flags", [DEC, PRE])
+def test_two_calls_and_two_graphs_at_once(flags):
+    """On two streams, each with outputs and workspaces of its own; then both captured, and replayed side by side."""
+    cases = [training_case(T=90, seed=1), training_case(T=70, seed=2)]
+    run = [lambda c=c: feed_forward(c[0], c[2], c[3], c[4], c[5], c[6], flags) for c in cases]
+    want = [f() for f in run]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run[i]())
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for out in got[i] for a, b in zip(out, want[i]))
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], [None, None]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            outs[i] = run[i]()
+    for _ in range(3):
+        for i in range(2):
+            for t in outs[i]:
+                t.zero_()
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i]))
 
 
 def test_decode_step_beside_the_fp4_layer():
