@@ -501,17 +501,16 @@ __device__ __forceinline__ void step(Ctx& c, Cursor& k, Addr& ad, Place& at, v4f
   at.load = next_half(load1);
 }
 
+// (Cached stores: non-temporal ones were 2 % slower for the sums, 16 experts of 8192
+// rows, K 2048, N 7168, 1886 us against 1936, and 12 % in the backward pass, 32 experts of
+// 2048 rows, K 4096, N 1536, 554 against 620; its non-temporal loads another 2 %.)
 __device__ __forceinline__ void store16(void* p, v4u v) { *reinterpret_cast<global<v4u>*>((uintptr_t)p) = v; }
-__device__ __forceinline__ void nt_store16(void* p, v4u v) {
-  __builtin_nontemporal_store(v, reinterpret_cast<global<v4u>*>((uintptr_t)p));
-}
-__device__ __forceinline__ void nt_store8(void* p, uint32_t a, uint32_t b) {
-  __builtin_nontemporal_store(v2u{a, b}, reinterpret_cast<global<v2u>*>((uintptr_t)p));
+__device__ __forceinline__ void store8(void* p, uint32_t a, uint32_t b) {
+  *reinterpret_cast<global<v2u>*>((uintptr_t)p) = v2u{a, b};
 }
 
 // Sums as they are: a lane's pair of tiles is eight neighbouring columns of its
-// token, a quad of lanes (g = 0..3) 32.  (Non-temporal stores were 2 % slower: 16
-// experts of 8192 rows, K 2048, N 7168: 1886 us, 1936 with them.)
+// token, a quad of lanes (g = 0..3) 32.
 template <int S, bool kF32>
 __device__ __forceinline__ int store_sums(const Ctx& c, const v4f (&acc)[8][4], const Tile& t, int sub0, int tn) {
   constexpr size_t kB = kF32 ? 4 : 2;
@@ -561,10 +560,10 @@ __device__ __forceinline__ int store_glu(const Ctx& c, v4f (&acc)[8][4], const T
         for (int p = 0; p < 2; ++p) {
           const size_t at = (row0 + 16 * i) * N + col0 + 32 * p;
           const v4f a = acc[4 * p][i], b = acc[4 * p + 2][i], d = acc[4 * p + 1][i], e = acc[4 * p + 3][i];
-          nt_store16(gate + at, v4u{f32x2_to_bf16(a[0], a[1]), f32x2_to_bf16(a[2], a[3]), f32x2_to_bf16(b[0], b[1]),
-                                    f32x2_to_bf16(b[2], b[3])});
-          nt_store16(up + at, v4u{f32x2_to_bf16(d[0], d[1]), f32x2_to_bf16(d[2], d[3]), f32x2_to_bf16(e[0], e[1]),
-                                  f32x2_to_bf16(e[2], e[3])});
+          store16(gate + at, v4u{f32x2_to_bf16(a[0], a[1]), f32x2_to_bf16(a[2], a[3]), f32x2_to_bf16(b[0], b[1]),
+                                 f32x2_to_bf16(b[2], b[3])});
+          store16(up + at, v4u{f32x2_to_bf16(d[0], d[1]), f32x2_to_bf16(d[2], d[3]), f32x2_to_bf16(e[0], e[1]),
+                               f32x2_to_bf16(e[2], e[3])});
         }
       }
       uint32_t m = 0;
@@ -594,7 +593,7 @@ __device__ __forceinline__ int store_glu(const Ctx& c, v4f (&acc)[8][4], const T
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const v4f lo = acc[4 * p][i], hi = acc[4 * p + 2][i];
-          nt_store8(o + 32 * p, block_codes(lo[0], lo[1], lo[2], lo[3], k), block_codes(hi[0], hi[1], hi[2], hi[3], k));
+          store8(o + 32 * p, block_codes(lo[0], lo[1], lo[2], lo[3], k), block_codes(hi[0], hi[1], hi[2], hi[3], k));
         }
         if (q == 0 && (c.wave & 1) == 0) g->a.s[(size_t)tn * P + row0 + 16 * i] = k.scale;
       }
@@ -617,8 +616,8 @@ __device__ __forceinline__ int store_grad(const Ctx& c, v4f (&acc)[8][4], const 
     const size_t at = row_of(i) * N + 128 * nb + 8 * q;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      eg[i & 1][p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(g->a.gate + at + 32 * p));
-      eu[i & 1][p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(g->a.up + at + 32 * p));
+      eg[i & 1][p] = *reinterpret_cast<const global<v4u>*>((uintptr_t)(g->a.gate + at + 32 * p));
+      eu[i & 1][p] = *reinterpret_cast<const global<v4u>*>((uintptr_t)(g->a.up + at + 32 * p));
     }
   };
   if constexpr (S > 0) fetch(0);
@@ -648,9 +647,9 @@ __device__ __forceinline__ int store_grad(const Ctx& c, v4f (&acc)[8][4], const 
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const v4f lo = acc[2 * p][i], hi = acc[2 * p + 1][i];
-        nt_store8(o + 32 * p, block_codes(lo[0], lo[1], lo[2], lo[3], kg), block_codes(hi[0], hi[1], hi[2], hi[3], kg));
+        store8(o + 32 * p, block_codes(lo[0], lo[1], lo[2], lo[3], kg), block_codes(hi[0], hi[1], hi[2], hi[3], kg));
         const float* u = du + 8 * p;
-        nt_store8(o + N + 32 * p, block_codes(u[0], u[1], u[2], u[3], ku), block_codes(u[4], u[5], u[6], u[7], ku));
+        store8(o + N + 32 * p, block_codes(u[0], u[1], u[2], u[3], ku), block_codes(u[4], u[5], u[6], u[7], ku));
       }
       if (q == 0) {
         g->a.s[(size_t)nb * P + row] = kg.scale;
