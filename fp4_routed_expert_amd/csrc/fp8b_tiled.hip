@@ -31,6 +31,14 @@
 //
 // The workgroups are persistent: one per CU (its LDS allows no second) walks its
 // XCD's contiguous share of the items, and the stages run on across items.
+//
+// 4604 rows, K 16384, N 7168: 440 us, 2.46 PFLOP/s, the MFMAs busy 61 % at the 1.8 GHz
+// that the power limit leaves.  A stage is 32 MFMAs of 32 clocks for each of a SIMD's
+// two waves and about 285 instructions, which take a wave eight clocks each: 2048
+// clocks of the matrix cores beside 2280 of each wave's issue, and what a wave waits at
+// the barriers on top.  With K 2048 an item is 16 stages and its stores 7 % of
+// it (16 experts of 8192 rows: 1886 us, 1758 with nothing stored).  SwiGLU of 256
+// experts of 144 rows, K 7168, N 2048: 1.43-1.54 ms, 7.8 GB at 5.2-5.6 TB/s.
 #include "fp8b.h"
 #include "tiled.h"
 
