@@ -8,7 +8,9 @@
 // Bound by HBM: 2 (or 4) bytes in and 1 + 1/32 out per element.  Sixteen lanes
 // take a block, eight elements each (one or two 128-bit loads), and join their
 // maxima by lane swaps; a workgroup takes 16 rows, so that the scales of a block,
-// held side by side for neighbouring rows, leave as runs of 64 bytes.
+// held side by side for neighbouring rows, leave as runs of 64 bytes.  16384 x 7168
+// bf16: 60 us, 5.9 TB/s; read back 53 us, 6.7 TB/s (a copy of 1 GiB: 5.15); 8 x 7168: 3.2
+// and 2.6 us.
 #include "fp8b.h"
 
 namespace moe {

@@ -76,7 +76,10 @@ __host__ __device__ __forceinline__ int tile_height(int n, int tiles) {
 }
 
 // How long tiles x ntn items take whose rows are at most 64 s: they run in rounds
-// of one per CU.  The s of the fewest units is taken, the largest on a tie.
+// of one per CU.  The s of the fewest units is taken, the largest on a tie (us, with s 4
+// always: K 7168, N 2048, 1024 rows 44 and 79; K 16384, N 7168, 512 rows 116 and 170; K
+// 4096, N 1536, 5000 rows 37 and 51; 4 experts of 256 rows, K 7168, N 2048, 47 and 82;
+// with 0, 2 or 7 for the 4 units of an item that do not shrink the same within 1 %).
 __host__ __device__ __forceinline__ float item_units(uint32_t tiles, int ntn, float per_cu, int s) {
   return ceilf((float)tiles * (float)ntn * per_cu) * (float)(4 + 2 * s);  // per_cu: 1 / CUs
 }
@@ -789,6 +792,12 @@ size_t fp8b_tiled_ws_bytes(long P, int E) { return rows_at(P, E) + 4 * (size_t)P
 hipError_t launch_fp8b_tiled(const Fp8bArgs& a, const Fp8bLayout& L, Fp8bOut out, void* ws, hipStream_t st) {
   const int ntn = (L.NT + kBT - 1) / kBT;
   const int most = out == Fp8bOut::kFp32 ? kWideSubs : 4;
+  // Where a group is a tile on average its weights are read once whatever the walk, and
+  // one panel keeps its rows in L2 (us, one panel and four, 256 experts of 144 rows, K
+  // 7168, N 2048: SwiGLU 1560 and 1570, its backward pass 889 and 894; 64 experts of 96
+  // rows, K 4096, N 1536, 151 and 155); else panels share weights between row tiles
+  // (T16384 to 256 experts, skewed, K 2048, N 7168: 2338 and 2165; dense, 4604 rows, K
+  // 16384, N 7168, 455 and 437; two, six, seven, eight and fourteen panels 0-5 % slower).
   Launch g{a, L, nullptr, nullptr, 0, 0, a.offsets && a.P <= kBM * (long)L.E ? 1 : 4};
   if (a.offsets) {
     int32_t* list = static_cast<int32_t*>(ws);
