@@ -17,8 +17,8 @@ constexpr int kMaxE = 1024;
 // A tile past the last row still counts in 32 bits; the streaming product's passes step by next_pass.
 constexpr int kMaxP = INT32_MAX - 256;
 
-// One workgroup of 256 threads per 16 rows and 4 blocks: the grid stays below 2^32 threads in each dimension.
-bool too_many(int32_t M, int32_t K) { return M > kMaxP / 16 * 16 || K > (1 << 20); }
+// (one workgroup per 16 rows and 4 blocks)
+bool too_many(int32_t M, int32_t K) { return M > kMaxP || K > (1 << 20); }
 
 moe_status_t check_enk(int32_t E, int32_t N, int32_t K, int32_t glu) {
   if (E < 1 || N < 1 || K < 1 || (glu != 0 && glu != 1)) return MOE_ERR_INVALID_ARGUMENT;

@@ -20,6 +20,10 @@ constexpr int kThreads = 256;
 constexpr int kRows = 16;   // rows of a workgroup
 constexpr int kBlocks = 4;  // blocks of a row that a thread takes, all loads in flight together
 
+// First row of a workgroup.  A launch dimension holds fewer than 2^32 threads, so the
+// rows run in x and z.
+__device__ __forceinline__ long first_row() { return ((long)blockIdx.z * gridDim.x + blockIdx.x) * kRows; }
+
 template <ElemType kT>
 struct Eight {
   v4u r[kT == ElemType::kFp32 ? 2 : 1];
@@ -62,7 +66,7 @@ template <ElemType kT>
 __global__ __launch_bounds__(kThreads) void quant_kernel(const uint8_t* __restrict__ x, long M, int J, long ld_bytes,
                                                          uint8_t* __restrict__ q, float* __restrict__ s) {
   constexpr int kBytes = kT == ElemType::kFp32 ? 32 : 16;
-  const long row = (long)blockIdx.x * kRows + (threadIdx.x >> 4);
+  const long row = first_row() + (threadIdx.x >> 4);
   const int j0 = (int)blockIdx.y * kBlocks, lane = threadIdx.x & 15;
   const bool live = row < M;
   const uint8_t* src = x + (live ? row : M - 1) * ld_bytes + lane * kBytes;
@@ -84,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(const uint8_t* __restri
 template <bool kGrad>
 __global__ __launch_bounds__(kThreads) void rows_kernel(const float* __restrict__ h, Fp8bArgs a, int E, int N) {
   const int lane = threadIdx.x & 15;
-  long row = (long)blockIdx.x * kRows + (threadIdx.x >> 4);
+  long row = first_row() + (threadIdx.x >> 4);
   const int j = (int)blockIdx.y, J = N / 128;
   int begin = 0, end = a.P;
   if (a.offsets) {
@@ -121,7 +125,7 @@ template <ElemType kT>
 __global__ __launch_bounds__(kThreads) void dequant_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s,
                                                            long M, int J, uint8_t* __restrict__ out) {
   constexpr int kBytes = kT == ElemType::kFp32 ? 32 : 16;
-  const long row = (long)blockIdx.x * kRows + (threadIdx.x >> 4);
+  const long row = first_row() + (threadIdx.x >> 4);
   const int j0 = (int)blockIdx.y * kBlocks, lane = threadIdx.x & 15;
   if (row >= M) return;
   uint2 c[kBlocks];
@@ -235,7 +239,11 @@ __global__ __launch_bounds__(kThreads) void pack_scales_kernel(const float* __re
   }
 }
 
-dim3 rows_grid(long M, int by) { return dim3((unsigned)((M + kRows - 1) / kRows), (unsigned)by); }
+dim3 rows_grid(long M, int by) {
+  constexpr long kX = 1 << 20;
+  const long n = (M + kRows - 1) / kRows;
+  return dim3((unsigned)(n < kX ? n : kX), (unsigned)by, (unsigned)((n + kX - 1) / kX));
+}
 dim3 pack_grid(size_t n) { return dim3((unsigned)(n < kPackX ? n : kPackX), (unsigned)((n + kPackX - 1) / kPackX)); }
 
 }  // namespace

@@ -35,7 +35,8 @@ extern "C" {
  * each one fp32 operation.  A block that holds a NaN or an infinity gets a NaN
  * scale and zero codes.
  *   x [M, K] of x_type (bf16, fp16 or fp32), rows ldx elements apart,
- *     ldx >= K, 16-byte aligned as is every row; K % 128 == 0
+ *     ldx >= K, 16-byte aligned as is every row; K % 128 == 0, K <= 2^20,
+ *     M < 2^31 - 256
  *   q [M, K] (out, 8-byte aligned), s [K/128, M] (out)
  */
 moe_status_t moe_quant_fp8_block(const void* x, int32_t x_type, int32_t M, int32_t K, int64_t ldx, uint8_t* q,
@@ -45,7 +46,7 @@ moe_status_t moe_quant_fp8_block(const void* x, int32_t x_type, int32_t M, int32
  * The values of such rows: code * scale, one fp32 product, rounded to nearest
  * even in bf16 and fp16.
  *   q [M, K] (8-byte aligned), s [K/128, M]; out [M, K] of out_type (16-byte
- *   aligned); K % 128 == 0
+ *   aligned); M and K as above
  */
 moe_status_t moe_dequant_fp8_block(const uint8_t* q, const float* s, int32_t M, int32_t K, void* out,
                                    int32_t out_type, hipStream_t stream);

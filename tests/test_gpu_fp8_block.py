@@ -74,6 +74,23 @@ def test_quant_strided_rows_and_views():
     assert q.shape == (0, 256) and s.shape == (2, 0)
 
 
+def test_quant_more_than_2_to_28_rows():
+    """More workgroups than a launch dimension holds threads for."""
+    M = 2 ** 28 + 2 ** 24 + 5
+    x = torch.zeros(M, 128, dtype=BF, device="cuda")
+    at = torch.tensor([0, 2 ** 24 - 1, 2 ** 24, 2 ** 28 - 1, 2 ** 28, M - 1], device="cuda")
+    rows = normal(gen(51), 6, 128).to(BF)
+    x[at] = rows
+    q, s = moe.quant_fp8_block(x)
+    want = ref.quant(rows)
+    assert torch.equal(q[at], want[0]) and torch.equal(s[:, at], want[1])
+    assert int((s != 2.0 ** -110 / 448).sum()) == 6
+    moe.dequant_fp8_block(q, s, out=x)
+    assert torch.equal(x[at].double(), ref.rows(*want).to(BF).double())
+    del x, q, s
+    torch.cuda.empty_cache()
+
+
 def test_quant_codes_of_torchs_type():
     x = normal(gen(8), 4, 256)
     q = torch.empty(4, 256, dtype=torch.float8_e4m3fn, device="cuda")
