@@ -49,10 +49,10 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 
 // 2048, 6 rows 99 and 100, 12 rows 125 and 103), or while streaming makes at most 2048
 // passes of 32 rows over a weight tile, eight per CU: the tiled product has few items
 // then.  Dense: K 4096 N 1536, 512 rows (1536 passes) 20 and 27, 768 rows (2304) 30
-// and 27; K 16384 N 7168, 128 rows (1792) 100 and 119, 160 rows (2240) 125 and 116; K
-// 7168 N 2048, 512 rows (2048) 42 and 42.  Where the sums stay in fp32 up to 3328: K
-// 16384 N 7168, 192 rows (2688) 161 and 186, 256 rows (3584) 197 and 185; K 1536 N
-// 4096, 512 rows (4096) 21 and 24.  Grouped, where the tiled product lists its tiles
+// and 27; K 16384 N 7168, 128 rows (1792) 80 and 120, 160 rows (2240) 125 and 116; K
+// 7168 N 2048, 512 rows (2048) 38 and 43.  Where the sums stay in fp32 up to 3584: K
+// 16384 N 7168, 256 rows (3584) 171 and 187; K 2048 N 7168, 256 rows 26 and 30, 333 rows
+// (4928) 33 and 31.  Grouped, where the tiled product lists its tiles
 // first, up to 2400 (a group's last pass counted half): 8 experts, K 512 N 512, 2048
 // rows (2176) 7.4 and 11.8; 16 experts, K 2048 N 512, 2000 rows (2240) 20 and 20; 30
 // experts, K 1024 N 1024, 1000 rows (2944) 14 and 14; 8 experts, K 4096 N 4096, 512
@@ -67,7 +67,7 @@ int choose_path(int64_t P, const Fp8bLayout& L, Fp8bOut out, bool grouped, uint3
   if (fd) return 0;
   if (fp) return 1;
   const int64_t rows = out == Fp8bOut::kGluGrad ? 6 : 12;
-  const int64_t most = out == Fp8bOut::kFp32 ? 3328 : grouped ? 2400 : 2048;
+  const int64_t most = out == Fp8bOut::kFp32 ? 3584 : grouped ? 2400 : 2048;
   const int64_t passes = grouped ? P / 32 + (L.E + 1) / 2 : (P + 31) / 32;
   return P <= rows * L.E || passes * L.NT <= most ? 0 : 1;
 }

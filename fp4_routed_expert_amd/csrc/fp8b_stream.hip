@@ -210,6 +210,13 @@ void stream_as(const Fp8bArgs& a, const Fp8bLayout& L, hipStream_t st) {
 //   7168, 32 rows: 27 against 30 with four waves; K 7168, N 2048, 256 rows: 23 and 23.
 //   With exact products (whose operands take more registers) and more pairs than
 //   CUs by four: K 4096, N 1536, 333 rows 18 against 21.
+// - Four token tiles to a pass, of one group, where that saves enough rounds of
+//   workgroups on the CUs: such a pass takes 1.5-1.7 times as long.  (Rounds of two
+//   and of four tiles, us: K 4096, N 4096, 64 rows, 1 and 1, 8.6 and 12.9; 128 rows, 2 and
+//   1, 14.4 and 12.9; 192 rows, 3 and 2, 20.3 and 23.4; K 16384, N 7168, 64 rows, 2 and 1,
+//   51 and 42; 128 rows, 4 and 2, 100 and 80; in fp32 56 and 46, 108 and 87.)  Below K
+//   4096 the rounds of small workgroups overlap, so one round only: K 2048, N 2048, 160
+//   rows, 2 and 1, 8.3 and 7.9; N 7168, 256 rows, 7 and 4, 26.0 and 27.6.
 // The counts are against the 256 CUs that these were measured on; a device with
 // fewer gets the same results.
 template <Fp8bOut kOut>
@@ -219,6 +226,14 @@ void stream_for(const Fp8bArgs& a, const Fp8bLayout& L, hipStream_t st) {
   const long groups = a.offsets ? min((long)L.E, (long)a.P) : 1;
   if (a.P > 16 * groups) {
     const long passes = a.offsets ? groups : (a.P + 31) / 32;
+    if constexpr (!kGlu) {
+      const long wide = (a.P + 63) / 64;
+      auto rounds = [&](long passes) { return (passes * (L.NT / 2) + kCUs - 1) / kCUs; };
+      if (!a.offsets && 17 * rounds(wide) < 10 * rounds(passes) && (L.J >= 32 || rounds(wide) == 1)) {
+        stream_as<8, 2, 4, 2, kOut>(a, L, st);
+        return;
+      }
+    }
     if (kOut == Fp8bOut::kFp32 && passes * L.NT > 2 * kCUs)
       stream_as<4, 2, 2, 2, kOut>(a, L, st);
     else

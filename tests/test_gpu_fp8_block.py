@@ -102,7 +102,7 @@ def test_quant_codes_of_torchs_type():
 @pytest.mark.parametrize("flags", [DEC, PRE])
 @pytest.mark.parametrize("dtype", [BF, FS])
 @pytest.mark.parametrize("T,K,N", [(1, 128, 32), (3, 256, 160), (16, 384, 128), (17, 128, 288), (40, 1024, 256),
-                                   (257, 640, 352), (600, 256, 512)])
+                                   (257, 640, 352), (600, 256, 512), (50, 384, 5120), (230, 4096, 4096)])
 def test_dense(flags, dtype, T, K, N):
     g = gen(T * 7 + K + N)
     xq, xs = make_rows(g, T, K)
