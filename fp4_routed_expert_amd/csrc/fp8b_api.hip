@@ -41,7 +41,7 @@ moe_status_t check_weights(const moe_fp8_block_weights_t* w, int32_t glu) {
 // The tiled product addresses activation rows by 32-bit byte offsets.
 bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 << 32) - 4096; }
 
-// 0: stream the weights, 1: tiled, -1: bad flags.  By default the weights are
+// The rows up to which a call streams the weights by default: they are
 // streamed while the groups average at most 12 rows (us, streaming against tiled, 64
 // experts: SwiGLU K 4096 N 1536, 6 rows 119 and 142, 12 rows 145 and 146, 24 rows 181
 // and 148; 256 experts, K 7168 N 2048, 8 rows 1202 and 1277, 16 rows 1830 and 1320),
@@ -61,30 +61,46 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 
 // group's rows 16 or 32 at a time, by one workgroup per tile pair once the groups'
 // tiles fill the CUs.  A caller that knows its routing to be skewed forces the tiled
 // product.
+int64_t streamed_rows(const Fp8bLayout& L, Fp8bOut out, bool grouped) {
+  const int64_t rows = out == Fp8bOut::kGluGrad ? 6 : 12;
+  const int64_t most = out == Fp8bOut::kFp32 ? 3584 : grouped ? 2400 : 2048;
+  // P / 32 + (E + 1) / 2 passes of groups, or P / 32 rounded up of one, times NT at most `most`
+  const int64_t passes = most / L.NT;
+  const int64_t few = grouped ? 32 * (passes - (L.E + 1) / 2) + 31 : 32 * passes;
+  return few > rows * L.E ? few : rows * L.E;
+}
+
+// 0: stream the weights, 1: tiled, -1: bad flags.
 int choose_path(int64_t P, const Fp8bLayout& L, Fp8bOut out, bool grouped, uint32_t flags) {
   const bool fd = flags & MOE_FLAG_FORCE_DECODE, fp = flags & MOE_FLAG_FORCE_PREFILL;
   if ((flags & ~(MOE_FLAG_FORCE_DECODE | MOE_FLAG_FORCE_PREFILL)) != 0 || (fd && fp)) return -1;
   if (fd) return 0;
   if (fp) return 1;
-  const int64_t rows = out == Fp8bOut::kGluGrad ? 6 : 12;
-  const int64_t most = out == Fp8bOut::kFp32 ? 3584 : grouped ? 2400 : 2048;
-  const int64_t passes = grouped ? P / 32 + (L.E + 1) / 2 : (P + 31) / 32;
-  return P <= rows * L.E || passes * L.NT <= most ? 0 : 1;
+  return P <= streamed_rows(L, out, grouped) ? 0 : 1;
 }
 
 size_t tiled_bytes(int32_t P, int32_t E) { return PackedLayout::align256(fp8b_tiled_ws_bytes(P, E)); }
 
 // Workspace of the calls whose rows are quantised: where the weights are streamed, fp32 rows.
-size_t rows_bytes(int32_t P, const Fp8bLayout& L, int path) {
-  return path == 0 ? PackedLayout::align256((size_t)P * L.N * 4) : tiled_bytes(P, L.E);
+size_t rows_bytes(int64_t P, const Fp8bLayout& L, int path) {
+  return path == 0 ? PackedLayout::align256((size_t)P * L.N * 4) : tiled_bytes((int32_t)P, L.E);
+}
+
+// The same for P rows or fewer.  (Few rows that are streamed need more than many that are not, and a program keeps
+// one workspace for both: 256 experts, N 2048, flags 0, 3072 rows 25 MB, 3073 rows by themselves 18 KB.)
+size_t rows_bytes_up_to(int64_t P, const Fp8bLayout& L, Fp8bOut out, uint32_t flags) {
+  const int path = choose_path(P, L, out, true, flags);
+  const size_t own = rows_bytes(P, L, path);
+  if (path == 0 || flags != 0) return own;
+  const size_t streamed = rows_bytes(streamed_rows(L, out, true), L, 0);
+  return own > streamed ? own : streamed;
 }
 
 // One size for the forward and the backward call, which may take different paths (twice the tiles with gate and up).
 size_t glu_bytes(int32_t P, int32_t E, int32_t N, int32_t K, uint32_t flags) {
   const Fp8bLayout one(E, N, K, false), two(E, N, K, true);
-  const int p1 = choose_path(P, one, Fp8bOut::kGluGrad, true, flags), p2 = choose_path(P, two, Fp8bOut::kGlu, true, flags);
-  if (p1 < 0 || p2 < 0) return 0;
-  const size_t a = rows_bytes(P, one, p1), b = rows_bytes(P, two, p2);
+  if (choose_path(P, one, Fp8bOut::kGluGrad, true, flags) < 0) return 0;
+  const size_t a = rows_bytes_up_to(P, one, Fp8bOut::kGluGrad, flags), b = rows_bytes_up_to(P, two, Fp8bOut::kGlu, flags);
   return a > b ? a : b;
 }
 
@@ -144,7 +160,7 @@ moe_status_t gated(const moe_fp8_block_weights_t* w, Fp8bOut out, const uint8_t*
   if (!xq || !xs || !q || !s || (gate == nullptr) != (up == nullptr) || (grad && !gate)) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(q, 8) || !aligned(s, 4) || !aligned(gate, 16) || !aligned(up, 16))
     return MOE_ERR_INVALID_ARGUMENT;
-  if (!workspace || workspace_bytes < glu_bytes(P, w->E, w->N, w->K, flags)) return MOE_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < rows_bytes(P, L, path)) return MOE_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
   const Fp8bArgs a{static_cast<const uint8_t*>(w->packed), xq, xs, X, offsets, rows, row_div, P, nullptr, q, s, gate, up};
   return run(a, L, path, out, workspace, stream);

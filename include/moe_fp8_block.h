@@ -142,7 +142,8 @@ moe_status_t moe_fp8_block_grouped_forward(const moe_fp8_block_weights_t* w /*(h
  *     pass, or both null
  *   Rows outside [offsets[0], offsets[E]) are left as they were in all outputs.
  *   workspace >= moe_fp8_block_glu_workspace_size(P, E, N, K, flags) bytes,
- *     256-byte aligned, as above
+ *     256-byte aligned, as above.  The size serves this call and the backward one,
+ *     for P rows and for any fewer of them, under the same flags.
  */
 size_t moe_fp8_block_glu_workspace_size(int32_t P, int32_t E, int32_t N, int32_t K, uint32_t flags);
 moe_status_t moe_fp8_block_glu_forward(const moe_fp8_block_weights_t* w /*(host)*/, const uint8_t* xq,

@@ -683,3 +683,21 @@ def test_decode_step_beside_the_fp4_layer():
             want[t] += float(gates[t, j]) * (ref.weights(m["w2"][0][e], m["w2"][1][e]) @ h[0])
     # h is off by half an e4m3 step (2^-4) at most, o by half a bf16 step
     assert (y.double() - want).norm() < (2.0 ** -4 + 2.0 ** -8) * want.norm()
+
+
+def test_one_workspace_for_a_large_batch_and_smaller_ones():
+    """The size for rows that take the tiled product serves fewer rows, which are streamed through it."""
+    g = gen(12)
+    E, N, K = 8, 512, 256
+    large = 2400
+    w13 = moe.fp8_block_prepack_glu(*make_weights(g, E, N, K), *make_weights(g, E, N, K))
+    w2_t = moe.fp8_block_prepack_t(*make_weights(g, E, K, N))
+    ws = torch.empty(moe.fp8_block_glu_workspace_size(large, E, N, K), dtype=torch.uint8, device="cuda")
+    for P in (large, 2309, 2200, 700, 40, 1):
+        off = torch.linspace(0, P, E + 1, device="cuda").int()
+        xq, xs = make_rows(g, P, K)
+        got = moe.fp8_block_glu(w13, xq, xs, off, save=True, workspace=ws)
+        want = moe.fp8_block_glu(w13, xq, xs, off, save=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), P
+        back = moe.fp8_block_glu_backward(w2_t, xq, xs, *got[2:], off, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(back, moe.fp8_block_glu_backward(w2_t, xq, xs, *got[2:], off))), P
