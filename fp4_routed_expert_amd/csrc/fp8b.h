@@ -114,10 +114,12 @@ __device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
 }
 
 // Backward of silu(g) u for the gradient dh: dg and du.  sig = 1 / (1 + e^-g) as
-// in glu_out (mx4.h); 1 - sig keeps its precision near 1 as e^-g sig.
+// in glu_out (mx4.h); 1 - sig keeps its precision near 1 as e^-g sig.  Below g =
+// -87.3 sig is 0, as |g| e^g < 2^-118 is: a sig that stays at 2^-126 would be
+// multiplied by gates of any size.
 __device__ __forceinline__ void glu_grad(float dh, float g, float u, float& dg, float& du) {
   const float t = __builtin_amdgcn_exp2f(fminf(g * -1.44269504f, 126.0f));  // e^-g
-  const float sig = __builtin_amdgcn_rcpf(1.0f + t);
+  const float sig = t < 0x1p126f ? __builtin_amdgcn_rcpf(1.0f + t) : 0.0f;
   du = dh * (g * sig);
   dg = dh * u * (sig * (1.0f + g * (t * sig)));
 }

@@ -155,8 +155,8 @@ moe_status_t moe_fp8_block_glu_forward(const moe_fp8_block_weights_t* w /*(host)
  * Backward of h = silu(g) u behind the backward of the down projection, grouped
  * as above: dh[s] = W2[e]^T dO[r(s)], sig = 1 / (1 + e^-g),
  *   dg = dh u sig (1 + g (1 - sig)),  du = dh g sig
- * in fp32 (sig from the hardware's exponential and reciprocal), quantised in
- * blocks of 128 of each.  [dg, du] are the rows of the input gradient's product
+ * in fp32 (sig from the hardware's exponential and reciprocal; 0 below g = -87.3,
+ * where |g| sig < 2^-118), quantised in blocks of 128 of each.  [dg, du] are the rows of the input gradient's product
  * (moe_fp8_block_prepack_t of both projections) and of the weight gradient.
  *   w plain, from moe_fp8_block_prepack_t of W2 [E, K, N]: N the block's inner
  *     width, N % 128 == 0

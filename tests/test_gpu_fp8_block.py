@@ -451,6 +451,31 @@ def test_glu_backward(flags, name, K, N):
         within(v[:, N:], du, ref.held(du, au), f"du, expert {e}")
 
 
+@pytest.mark.parametrize("flags", [DEC, PRE])
+def test_glu_backward_gates_of_all_sizes(flags):
+    """Gates up to the ends of bf16, each in a block of its own.  Below -87.3 sig may be 0, which leaves out |g| e^g <
+    2^-118; blocks of so small values have the least scale there is.  Past 100 the exponential's argument, whose
+    rounding grows with g, no longer matters."""
+    g = gen(61)
+    sizes = [-3e38, -1e38, -1e30, -1e20, -1e5, -1e3, -200.0, -100.0, -88.0, -87.5, -87.0, -80.0, -20.0, -1.5, -1e-30, 0.0,
+             1e-30, 2.0, 50.0, 90.0, 1e4, 1e20, 1e30]
+    P, K, N = len(sizes), 128, 128
+    yq, ys = make_rows(g, P, K)
+    wq, ws = make_weights(g, 1, K, N)
+    gate = torch.tensor(sizes, device="cuda").to(BF).unsqueeze(1).repeat(1, N)
+    up = normal(g, P, N).to(BF)
+    q, s = moe.fp8_block_glu_backward(moe.fp8_block_prepack_t(wq[0], ws[0]), yq, ys, gate, up, flags=flags)
+    dh, adh = ref.product(ref.rows(yq, ys), ref.weights(wq[0], ws[0]).T.contiguous())
+    sig, gd, ud = torch.sigmoid(gate.double()), gate.double(), up.double()
+    rel = (gd.abs().clamp(max=100) + 8) * 2.0 ** -22
+    slope, big, tiny = sig * (1 + gd * (1 - sig)), dh.abs() + adh, 2.0 ** -118
+    bend = sig * (1 + gd.abs() * (1 - sig)) * 3 * rel + slope.abs() * 2.0 ** -21 + tiny
+    dg, du = dh * ud * slope, dh * gd * sig
+    v, least = ref.rows(q, s), 2.0 ** -110 / 448 * 2.0 ** -10
+    within(v[:, :N], dg, ref.held(dg, adh * (ud * slope).abs() + big * ud.abs() * bend) + least, "dg")
+    within(v[:, N:], du, ref.held(du, adh * (gd * sig).abs() + big * ((gd * sig).abs() * 2 * rel + tiny)) + least, "du")
+
+
 def test_glu_grad_against_differences():
     """The formula that the kernel is tested against is the derivative of silu(g) u."""
     g, u = torch.linspace(-6, 6, 49, dtype=torch.float64), torch.linspace(2, -3, 49, dtype=torch.float64)
