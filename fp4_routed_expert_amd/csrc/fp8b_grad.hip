@@ -4,10 +4,13 @@
 // The sum runs over rows, along which both scales vary, so the products are made
 // in the fp16 matrix cores (the rate of bf16, three bits more).  x's codes are
 // exact in fp16; dy's codes are multiplied by both scales.  The scales' products are
-// divided first by a power of two that brings that of the group's largest ones to
-// [2^4, 2^6), so that the range of fp16 costs little: a product's two roundings, of the
-// scale and of the product, are 2^-10 of it, and where the scales are less than 2^-18 of
-// the largest ones 2^-29 of what those would make.  The sums are fp32.
+// divided first by a power of two that brings the largest of the group's rows to [2^4,
+// 2^6), so that the range of fp16 costs little: a row's two roundings, of the
+// scales' product and of the code times it, are 2^-10 of it, and where its scales'
+// product is less than 2^-18 of the largest row's 2^-29 of what that would make.  (The
+// largest product of a row, not that of the largest dy and the largest x scale: an
+// outlier of each in different rows would cost the others their bits.)  The sums are
+// fp32.
 //
 // A workgroup makes 256 x 256 outputs of one expert, eight waves of 64 x 128 by
 // v_mfma_f32_32x32x16_f16, in steps of 32 rows.  The matrix cores want eight
@@ -115,6 +118,15 @@ __device__ __forceinline__ void each(F&& f, std::integer_sequence<int, I...>) {
   (f(std::integral_constant<int, I>{}), ...);
 }
 
+constexpr int kUp = 6;  // the scales' products are brought below 2^kUp, times 448 below 2^15
+
+// A scale's exponent: |v| < 2^exponent.  (What is below 2^-126, zeros too, counts as
+// 2^-126: fp16's normal numbers reach 2^-18 below the largest row.  A NaN or an
+// infinity shows in the outputs whatever they are divided by.)
+__device__ __forceinline__ int scale_exponent(float v) { return (int)((__float_as_uint(v) >> 23) & 255u) - 126; }
+// Maximum over a wave.
+__device__ __forceinline__ int wave_max_i32(int v) { return (int)(max_lanes_xor16_32_u32(row16_max_u32((uint32_t)v + 512u)) - 512u); }
+
 // What the loop is given.
 struct GradCtx {
   uint32_t lds0;
@@ -124,7 +136,7 @@ struct GradCtx {
   int width, tile;        // its columns, and the tile's place among them
   const float* scales;    // of the blocks that a dy wave moves
   const int32_t* xrows;
-  int up_y, up_x;         // powers of two for a dy wave's products
+  int up_y, up_x;         // powers of two for a dy wave's scales, whose products come to 2^kUp less
 };
 
 // The loop of a wave; it moves rows 8 o .. 8 o + 7 of every step of x (kIsX) or dy.
@@ -195,7 +207,7 @@ __device__ __forceinline__ void run_rows(const GradCtx& g, v16f (&acc)[4][2]) {
   };
   auto put_products = [&](int step, int slot) {
     if constexpr (!kIsX) {
-      float k = __builtin_amdgcn_ldexpf(fy, g.up_y) * __builtin_amdgcn_ldexpf(fx, g.up_x);
+      float k = __builtin_amdgcn_ldexpf(fy, g.up_y) * __builtin_amdgcn_ldexpf(fx, g.up_x) * (float)(1 << kUp);
       if (step >= steps - 1)  // rows past the last one
         k = (uint32_t)begin + (uint32_t)(kStepRows * step + (lane & 31)) <= last ? k : 0.0f;
       *reinterpret_cast<__attribute__((address_space(3))) _Float16*>((uintptr_t)(product_at + 256u * (slot & 1))) = (_Float16)k;
@@ -312,41 +324,42 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
   const int steps = (end - begin + kStepRows - 1) / kStepRows;
 
-  // The largest scales of the group's rows in the tile's blocks, as powers of two:
-  // y_exp and x_exp with scale < 2^exp.
+  // The largest product of scales of a row of the group, for each pair of the tile's
+  // blocks of dy and x, as a power of two: that of blocks i and j is below
+  // 2^top[2 i + j].
   const int nb0 = min(2 * tn, a.N / 128 - 1), nb1 = min(2 * tn + 1, a.N / 128 - 1);
   const int kb0 = min(2 * tk, a.K / 128 - 1), kb1 = min(2 * tk + 1, a.K / 128 - 1);
   auto x_row = [&](int s) { return kGather ? g.xrows[s] : s; };
-  int y_exp[2], x_exp[2];
+  int top[4] = {-252, -252, -252, -252};
   {
     const float* p[4] = {a.ys + (size_t)nb0 * a.P, a.ys + (size_t)nb1 * a.P, a.xs + (size_t)kb0 * a.X,
                          a.xs + (size_t)kb1 * a.X};
-    float top[4] = {0.f, 0.f, 0.f, 0.f};
     for (long first = begin + tid; first < end; first += 4 * 512) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int s = (int)min(first + 512 * u, (long)end - 1), x = x_row(s);
+        int exp[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], fabsf(p[i][i < 2 ? s : x]));
+        for (int i = 0; i < 4; ++i) exp[i] = scale_exponent(p[i][i < 2 ? s : x]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = max(top[i], exp[i >> 1] + exp[2 + (i & 1)]);
       }
     }
-    float(*tops)[4] = reinterpret_cast<float(*)[4]>(lds + kOffTop);
+    int(*tops)[4] = reinterpret_cast<int(*)[4]>(lds + kOffTop);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float m = max_lanes_xor16_32(row16_max(top[i]));
+      const int m = wave_max_i32(top[i]);
       if (lane == 0) tops[wave][i] = m;
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float m = 0.0f;
+      int m = tops[0][i];
 #pragma unroll
-      for (int w = 0; w < 8; ++w) m = fmaxf(m, tops[w][i]);
-      const int exp = (int)wave_u32((uint32_t)__builtin_amdgcn_frexp_expf(m));
-      (i < 2 ? y_exp[i & 1] : x_exp[i & 1]) = exp;
+      for (int w = 1; w < 8; ++w) m = max(m, tops[w][i]);
+      top[i] = (int)wave_u32((uint32_t)m);
     }
   }
-  constexpr int kUp = 6;  // the scales' products are brought below 2^kUp, times 448 below 2^15
 
   const int wn = wave >> 1, wk = wave & 1;  // columns 64 wn of dy, 128 wk of x
   v16f acc[4][2];
@@ -367,12 +380,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       run_rows<true, kGather>(c, acc);
     } else {
       c.scales = o < 2 ? a.ys + (size_t)(o ? nb1 : nb0) * a.P : a.xs + (size_t)(o == 3 ? kb1 : kb0) * a.X;
-      c.up_y = -(o >> 1 ? y_exp[1] : y_exp[0]);
-      c.up_x = kUp - (o & 1 ? x_exp[1] : x_exp[0]);
+      // half to each scale: with exponents of -126 to 128 neither passes 2^128
+      const int t = o == 0 ? top[0] : o == 1 ? top[1] : o == 2 ? top[2] : top[3];
+      c.up_y = -t >> 1;
+      c.up_x = -t - c.up_y;
       run_rows<false, kGather>(c, acc);
     }
   }
-  const int down = (wn >> 1 ? y_exp[1] : y_exp[0]) + (wk ? x_exp[1] : x_exp[0]) - kUp;
+  const int down = (wn >> 1 ? (wk ? top[3] : top[2]) : (wk ? top[1] : top[0])) - kUp;
 
   // Element v of a lane: column n = lane % 32 of dy, column 8 (v / 4) + 4 (lane / 32) +
   // v % 4 of x.  They go through LDS (piece q of 16 bytes of row n at q ^ n), so that

@@ -175,9 +175,10 @@ moe_status_t moe_fp8_block_glu_backward(const moe_fp8_block_weights_t* w /*(host
  * Gradient of the weights: dw[e, n, k] = sum over the rows s of group e of
  * dy[s, n] x[r(s), k], both rows quantised.  Their scales vary along this sum,
  * so it runs in the fp16 matrix cores: x's codes are exact there; the product of
- * the two scales, relative to that of the largest ones of the group's rows, and dy's
- * code times it are rounded to fp16: 2^-10 of each product together, or, where the
- * scales are less than 2^-18 of the largest ones, 2^-29 of what those would make.
+ * a row's two scales, relative to the largest such product of the group's rows, and
+ * dy's code times it are rounded to fp16: 2^-10 of each product together, or, where a
+ * row's product of scales is less than 2^-18 of the largest one, 2^-29 of what that
+ * would make.
  * Sums in fp32, rounded once to dw_type (bf16, or fp32 as it is).  A group without
  * rows gets zeros.
  *   yq [P, N], ys [N/128, P]; xq [X, K], xs [K/128, X]; codes 16-byte aligned

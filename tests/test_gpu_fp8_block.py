@@ -556,6 +556,56 @@ def test_weight_grad_scales_of_all_sizes(parts):
         within(dw, want, err + grad_floor(y2, x2, P) + 2.0 ** -149, f"{low} {high}")
 
 
+def row_floor(ys, xs):
+    """What the range of fp16 may cost the rows' sums, [N, K]: n (2^-29 448 448 + 2^-29 448) times the largest product of
+    one row's scales."""
+    top = (ys.abs().double().unsqueeze(1) * xs.abs().double().unsqueeze(0)).amax(-1)
+    return ys.shape[1] * 2.0 ** -29 * (448 * 448 + 448) * top.repeat_interleave(128, 0).repeat_interleave(128, 1)
+
+
+@pytest.mark.parametrize("P", [60, 1500])
+@pytest.mark.parametrize("gather", [False, True])
+def test_weight_grad_outliers_in_different_rows(P, gather):
+    """A row of large gradients and another of large activations, whose codes are zero in half of the channels, leave
+    the other rows' bits alone: no row's scales are both large."""
+    g = gen(62)
+    for e in (0, 6, 12, 16, 20, 40):
+        y, x = normal(g, P, 384), normal(g, P, 256)
+        for n in range(0, 384, 128):
+            y[3, n:n + 64] = 0
+        for n in range(0, 256, 128):
+            x[5, n:n + 64] = 0
+        y[3] *= 2.0 ** e
+        x[5] *= 2.0 ** e
+        (yq, ys), (xq, xs) = moe.quant_fp8_block(y), moe.quant_fp8_block(x)
+        v = ref.rows(xq, xs)
+        off = torch.tensor([0, P], dtype=torch.int32, device="cuda")
+        if gather:  # an odd row of x stands for two neighbouring rows of dy
+            rows = torch.arange(P, device="cuda", dtype=torch.int32) // 2 * 2 + 1
+            dw = moe.fp8_block_weight_grad(yq, ys, xq, xs, off, rows=rows, dtype=FS)[0]
+            v, xs = v[rows.long()], xs[:, rows.long()]
+        else:
+            dw = moe.fp8_block_weight_grad(yq, ys, xq, xs, off, dtype=FS)[0]
+        want, err = grad_bound(ref.rows(yq, ys), v, ref.HALF[FS])
+        within(dw, want, err + row_floor(ys, xs), f"2^{e}")
+
+
+def test_weight_grad_scales_at_the_ends_of_fp32():
+    """One scale near 2^127 beside one near 2^-126 in a row, zeros, and scales below the normal numbers."""
+    g = gen(63)
+    P = 64
+    (yq, _), (xq, _) = make_rows(g, P, 128), make_rows(g, P, 128)
+    e = torch.linspace(-126, 126, P, device="cuda")
+    for lift in (0.0, -20.0, 20.0):
+        ys, xs = torch.exp2(e).unsqueeze(0), torch.exp2((lift - e).clamp(-126, 127)).unsqueeze(0)
+        xs[0, 7], ys[0, 50] = 0.0, 0.0
+        want, err = grad_bound(ref.rows(yq, ys), ref.rows(xq, xs), ref.HALF[FS])
+        within(moe.fp8_block_weight_grad(yq, ys, xq, xs, dtype=FS), want, err + row_floor(ys, xs), f"lift {lift}")
+    ys, xs = torch.full((1, P), 2.0 ** -135, device="cuda"), torch.full((1, P), 2.0 ** 100, device="cuda")
+    want, err = grad_bound(ref.rows(yq, ys), ref.rows(xq, xs), ref.HALF[FS])
+    within(moe.fp8_block_weight_grad(yq, ys, xq, xs, dtype=FS), want, err + row_floor(ys, xs), "subnormal")
+
+
 def test_weight_grad_all_codes():
     """Every code of e4m3, and the not-a-numbers where they belong: a row of dw and a column of it."""
     g = gen(32)
