@@ -44,10 +44,10 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 
 // The rows up to which a call streams the weights by default: they are
 // streamed while the groups average at most 12 rows (us, streaming against tiled, 64
 // experts: SwiGLU K 4096 N 1536, 6 rows 119 and 142, 12 rows 145 and 146, 24 rows 181
-// and 148; 256 experts, K 7168 N 2048, 8 rows 1202 and 1277, 16 rows 1830 and 1320),
-// for the backward call, whose rows take a second launch then, at most 6 (K 4096 N
-// 2048, 6 rows 99 and 100, 12 rows 125 and 103), or while streaming makes at most 2048
-// passes of 32 rows over a weight tile, eight per CU: the tiled product has few items
+// and 148; 256 experts, K 7168 N 2048, 8 rows 1202 and 1277, 16 rows 1830 and 1320;
+// the backward call, 64 experts, K 4096 N 2048, 6 rows 86 and 102, 12 rows 90 and 102, 24
+// rows 111 and 104; 256 experts, K 7168 N 2048, 12 rows 619 and 644, 16 rows 665 and
+// 644), or while streaming makes at most 2048 passes of 32 rows over a weight tile, eight per CU: the tiled product has few items
 // then.  Dense: K 4096 N 1536, 512 rows (1536 passes) 20 and 27, 768 rows (2304) 30
 // and 27; K 16384 N 7168, 128 rows (1792) 80 and 120, 160 rows (2240) 125 and 116; K
 // 7168 N 2048, 512 rows (2048) 38 and 43.  Where the sums stay in fp32 up to 3584: K
@@ -62,12 +62,11 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 
 // tiles fill the CUs.  A caller that knows its routing to be skewed forces the tiled
 // product.
 int64_t streamed_rows(const Fp8bLayout& L, Fp8bOut out, bool grouped) {
-  const int64_t rows = out == Fp8bOut::kGluGrad ? 6 : 12;
   const int64_t most = out == Fp8bOut::kFp32 ? 3584 : grouped ? 2400 : 2048;
   // P / 32 + (E + 1) / 2 passes of groups, or P / 32 rounded up of one, times NT at most `most`
   const int64_t passes = most / L.NT;
   const int64_t few = grouped ? 32 * (passes - (L.E + 1) / 2) + 31 : 32 * passes;
-  return few > rows * L.E ? few : rows * L.E;
+  return few > 12 * L.E ? few : 12 * L.E;
 }
 
 // 0: stream the weights, 1: tiled, -1: bad flags.

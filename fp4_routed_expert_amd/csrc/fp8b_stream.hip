@@ -1,7 +1,7 @@
 // FP8 products with block scales of 128 for few rows: y[s, n] = sum over blocks
 // b of sx[b, r] sw[n / 128, b] (sum_{k in b} xq[r, k] wq[e, n, k]).  One MFMA
-// (K = 128) is one block's sum (four with exact products where the result stays in
-// fp32); the two scales meet it in one fp32 multiply-add per element, since they
+// (K = 128) is one block's sum (four with exact products where the result is fp32 for
+// the caller); the two scales meet it in one fp32 multiply-add per element, since they
 // are no powers of two.
 //
 // Weight streaming, bound by HBM: a workgroup owns two neighbouring weight
@@ -81,7 +81,9 @@ __device__ __forceinline__ void multiply(const Step<NT, TT>& p, v4f (&acc)[NT][T
 }
 
 // kOut: kBf16 and kFp32 write a.y; kGlu writes h to a.y as fp32 rows, and gate
-// and up where they are wanted.
+// and up where they are wanted; kGluGrad writes dh to a.y as fp32 rows, summed as what
+// is quantised behind it is (with exact products 64 experts of 6 rows, K 4096, N 2048,
+// take 100 us instead of 86).
 template <int NW, int NT, int TT, int kB, Fp8bOut kOut>
 __global__ __launch_bounds__(64 * NW) void stream_kernel(Fp8bArgs a, Fp8bLayout L) {
   constexpr bool kGlu = kOut == Fp8bOut::kGlu, kExact = kOut == Fp8bOut::kFp32;
@@ -263,7 +265,7 @@ hipError_t launch_fp8b_stream(const Fp8bArgs& args, const Fp8bLayout& L, Fp8bOut
   if (out == Fp8bOut::kGlu)
     stream_for<Fp8bOut::kGlu>(a, L, st);
   else
-    stream_for<Fp8bOut::kFp32>(a, L, st);
+    stream_for<Fp8bOut::kGluGrad>(a, L, st);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? e : launch_fp8b_rows(ws, args, L.E, L.N, out, st);
 }

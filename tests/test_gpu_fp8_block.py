@@ -476,6 +476,22 @@ def test_glu_backward_gates_of_all_sizes(flags):
     within(v[:, N:], du, ref.held(du, adh * (gd * sig).abs() + big * ((gd * sig).abs() * 2 * rel + tiny)) + least, "du")
 
 
+def test_glu_backward_sums_alike_either_way():
+    """Streamed or tiled, dh of one block of K is the same matrix instruction's sum, so that the codes are the same
+    bits: for every code, and where large products cancel and leave small ones, which those sums may drop."""
+    g = gen(64)
+    P, K, N = 75, 128, 256
+    wq = torch.randint(0, 256, (K, N), generator=g, device="cuda", dtype=torch.uint8)
+    yq = torch.randint(0, 256, (P, K), generator=g, device="cuda", dtype=torch.uint8)
+    wq[(wq & 127) == 127], yq[(yq & 127) == 127] = 0x7E, 0x80
+    wq[1::8], yq[40:, 1::8] = wq[::8], yq[40:, ::8] ^ 0x80
+    ys, ws = torch.rand(1, P, generator=g, device="cuda") + 0.1, torch.rand(1, 2, generator=g, device="cuda") + 0.1
+    gate, up = (2 * normal(g, P, N)).to(BF), normal(g, P, N).to(BF)
+    w = moe.fp8_block_prepack_t(wq, ws)
+    a, b = (moe.fp8_block_glu_backward(w, yq, ys, gate, up, flags=f) for f in (DEC, PRE))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_glu_grad_against_differences():
     """The formula that the kernel is tested against is the derivative of silu(g) u."""
     g, u = torch.linspace(-6, 6, 49, dtype=torch.float64), torch.linspace(2, -3, 49, dtype=torch.float64)
