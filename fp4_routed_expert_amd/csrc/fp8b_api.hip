@@ -47,8 +47,8 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 
 // and 148; 256 experts, K 7168 N 2048, 8 rows 1202 and 1277, 16 rows 1830 and 1320;
 // the backward call, 64 experts, K 4096 N 2048, 6 rows 86 and 102, 12 rows 90 and 102, 24
 // rows 111 and 104; 256 experts, K 7168 N 2048, 12 rows 619 and 644, 16 rows 665 and
-// 644), or while streaming makes at most 2048 passes of 32 rows over a weight tile, eight per CU: the tiled product has few items
-// then.  Dense: K 4096 N 1536, 512 rows (1536 passes) 20 and 27, 768 rows (2304) 30
+// 644), or while streaming makes at most 2048 passes of 32 rows over a weight tile,
+// eight per CU: the tiled product has few items then.  Dense: K 4096 N 1536, 512 rows (1536 passes) 20 and 27, 768 rows (2304) 30
 // and 27; K 16384 N 7168, 128 rows (1792) 80 and 120, 160 rows (2240) 125 and 116; K
 // 7168 N 2048, 512 rows (2048) 38 and 43.  Where the sums stay in fp32 up to 3584: K
 // 16384 N 7168, 256 rows (3584) 171 and 187; K 2048 N 7168, 256 rows 26 and 30, 333 rows
@@ -284,8 +284,9 @@ moe_status_t moe_fp8_block_weight_grad(const uint8_t* yq, const float* ys, const
   moe_status_t st = check_enk(E, N, K, 0);
   if (st != MOE_OK) return st;
   if (P < 0 || X < 0 || row_div < 1 || !sum_type(dw_type)) return MOE_ERR_INVALID_ARGUMENT;
-  // (one workgroup of 512 threads per 256 x 256 outputs, below 2^32 threads)
-  if (N % 128 != 0 || P > kMaxP || (int64_t)N * K >= (int64_t)1 << 39) return MOE_ERR_UNSUPPORTED;
+  // one workgroup of 512 threads per 256 x 256 outputs (a last tile may be half of one), in multiples of eight:
+  // below 2^32 threads
+  if (N % 128 != 0 || P > kMaxP || (int64_t)((N + 255) / 256) * ((K + 255) / 256) > (1 << 23) - 8) return MOE_ERR_UNSUPPORTED;
   if (!dw || !aligned(dw, 16)) return MOE_ERR_INVALID_ARGUMENT;
   if (P > 0) {
     st = check_rows(X, offsets, rows, P, E);

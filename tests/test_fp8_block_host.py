@@ -207,6 +207,14 @@ def test_weight_grad_refusals():
     assert call(nb=ws - 1) == WSE and call(w=NUL) == WSE and call(w=ctypes.c_void_p((1 << 20) + 16)) == INV
 
 
+@pytest.mark.parametrize("N,K", [(1 << 20, (1 << 19) - 128), ((1 << 19) - 128, 1 << 20)])
+def test_weight_grad_refuses_as_many_tiles_as_no_launch_holds(N, K):
+    """Half tiles count as whole ones: 2^23 workgroups of 512 threads are 2^32."""
+    size = L.moe_fp8_block_weight_grad_workspace_size(64, 1, N, K)
+    for P in (0, 64):
+        assert L.moe_fp8_block_weight_grad(A, A, A, A, 64, NUL, NUL, 1, P, 1, N, K, A, BF, A, size, NUL) == UNS
+
+
 def test_wrappers_refuse_host_tensors_and_wrong_shapes():
     u8, f32 = torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(2, 4)
     with pytest.raises(ValueError):
