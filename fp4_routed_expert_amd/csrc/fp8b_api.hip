@@ -86,7 +86,7 @@ size_t rows_bytes(int64_t P, const Fp8bLayout& L, int path) {
 }
 
 // The same for P rows or fewer.  (Few rows that are streamed need more than many that are not, and a program keeps
-// one workspace for both: 256 experts, N 2048, flags 0, 3072 rows 25 MB, 3073 rows by themselves 18 KB.)
+// one workspace for both: 250 experts, N 2048, flags 0, 3000 rows 25 MB, 3001 rows by themselves 18 KB.)
 size_t rows_bytes_up_to(int64_t P, const Fp8bLayout& L, Fp8bOut out, uint32_t flags) {
   const int path = choose_path(P, L, out, true, flags);
   const size_t own = rows_bytes(P, L, path);
