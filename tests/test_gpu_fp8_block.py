@@ -792,3 +792,207 @@ def test_one_workspace_for_a_large_batch_and_smaller_ones():
         assert all(torch.equal(a, b) for a, b in zip(got, want)), P
         back = moe.fp8_block_glu_backward(w2_t, xq, xs, *got[2:], off, workspace=ws)
         assert all(torch.equal(a, b) for a, b in zip(back, moe.fp8_block_glu_backward(w2_t, xq, xs, *got[2:], off))), P
+
+
+# -------------------------------------------- forms that only larger sizes take
+def tall_groups(low, high, seed, E=128):
+    """Ragged groups of low to high rows, every ninth empty: offsets, pairs (two a token), expert of each row."""
+    gc = torch.Generator().manual_seed(seed)
+    sizes = torch.randint(low, high + 1, (E,), generator=gc)
+    sizes[4::9] = 0
+    P = (int(sizes.sum()) + 7) // 2 * 2
+    off = torch.cat([torch.tensor([3]), 3 + sizes.cumsum(0)]).int().cuda()
+    expert = torch.full((P,), -1)
+    expert[3:3 + int(sizes.sum())] = torch.repeat_interleave(torch.arange(E), sizes)
+    return off, torch.randperm(P, generator=gc).int().cuda(), expert.cuda(), P, E
+
+
+def tile_rows(workspace):
+    """Rows of the tiles that the tiled product listed in its workspace."""
+    w = workspace.view(torch.int32)
+    return w[4:4 + 4 * int(w[0])].view(-1, 4)[:, 2]
+
+
+# rows of a group, and the heights of tile that they are to be cut to (three and four token tiles a wave)
+TALL = {"three": (110, 190, 129, 192), "four": (200, 256, 193, 256), "four, several tiles": (150, 700, 193, 256)}
+
+
+def assert_tall(workspace, name):
+    top = int(tile_rows(workspace).max())
+    assert TALL[name][2] <= top <= TALL[name][3], top
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("K", [128, 256, 384, 1152])
+@pytest.mark.parametrize("name", list(TALL))
+def test_grouped_tall_tiles(name, K, gather):
+    N = 1056
+    off, pair, expert, P, E = tall_groups(*TALL[name][:2], seed=K)
+    g = gen(K + 5)
+    xq, xs = make_rows(g, P // 2 if gather else P, K)
+    wq, ws = make_weights(g, E, N, K)
+    ws_ = torch.empty(moe.fp8_block_grouped_workspace_size(P, E, N, K), dtype=torch.uint8, device="cuda")
+    y = torch.full((P, N), 7.0, dtype=BF, device="cuda")
+    moe.fp8_block_grouped(moe.fp8_block_prepack(wq, ws), xq, xs, off, **({"rows": pair, "row_div": 2} if gather else {}),
+                          flags=PRE, y=y, workspace=ws_)
+    assert_tall(ws_, name)
+    x = ref.rows(xq, xs)
+    x = x[(pair // 2).long()] if gather else x
+    assert (y[expert < 0] == 7).all()
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        want, err = ref.product(x[a:b], ref.weights(wq[e], ws[e]), ref.HALF[BF])
+        within(y[a:b], want, err, f"expert {e}")
+
+
+@pytest.mark.parametrize("T", [2300, 3000])
+def test_dense_tall_tiles(T):
+    """Three and four token tiles a wave of one group (256 CUs: heights of 192 and 256 rows are the fewest rounds)."""
+    K, N = 384, 4096 + 96
+    g = gen(T)
+    xq, xs = make_rows(g, T, K)
+    wq, ws = make_weights(g, 1, N, K)
+    y = moe.fp8_block_dense(moe.fp8_block_prepack(wq[0], ws[0]), xq, xs, flags=PRE)
+    want, err = ref.product(ref.rows(xq, xs), ref.weights(wq[0], ws[0]), ref.HALF[BF])
+    within(y, want, err)
+
+
+@pytest.mark.parametrize("save", [False, True])
+@pytest.mark.parametrize("K", [128, 256, 384, 1152])
+@pytest.mark.parametrize("name", list(TALL))
+def test_gated_tall_tiles(name, K, save):
+    N = 512
+    off, pair, expert, P, E = tall_groups(*TALL[name][:2], seed=K + 1)
+    g = gen(K + 6)
+    xq, xs = make_rows(g, P // 2, K)
+    (wq, ws), (uq, us) = make_weights(g, E, N, K), make_weights(g, E, N, K)
+    x = ref.rows(xq, xs)[(pair // 2).long()]
+    q, s = torch.full((P, N), 9, dtype=torch.uint8, device="cuda"), torch.full((N // 128, P), 7.0, device="cuda")
+    room = torch.empty(moe.fp8_block_glu_workspace_size(P, E, N, K, PRE), dtype=torch.uint8, device="cuda")
+    gate, up = (torch.full((P, N), 7.0, dtype=BF, device="cuda") for _ in range(2)) if save else (None, None)
+    moe.fp8_block_glu(moe.fp8_block_prepack_glu(wq, ws, uq, us), xq, xs, off, rows=pair, row_div=2, flags=PRE, q=q, s=s,
+                      gate=gate, up=up, workspace=room)
+    assert_tall(room, name)
+    out = expert < 0
+    assert (q[out] == 9).all() and (s[:, out] == 7).all()
+    assert not save or ((gate[out] == 7).all() and (up[out] == 7).all())
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        if a < b:
+            (vg, eg), (vu, eu), (h, eh) = ref.glu(x[a:b], ref.weights(wq[e], ws[e]), ref.weights(uq[e], us[e]))
+            within(ref.rows(q[a:b], s[:, a:b]), h, ref.held(h, eh), f"expert {e}")
+            if save:
+                within(gate[a:b], vg, eg + ref.HALF[BF] * (vg.abs() + eg), "gate")
+                within(up[a:b], vu, eu + ref.HALF[BF] * (vu.abs() + eu), "up")
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("K", [128, 256, 384, 1152])
+@pytest.mark.parametrize("name", list(TALL))
+def test_glu_backward_tall_tiles(name, K, gather):
+    N = 896
+    off, pair, expert, P, E = tall_groups(*TALL[name][:2], seed=K + 2)
+    g = gen(K + 7)
+    yq, ys = make_rows(g, P // 2 if gather else P, K)
+    wq, ws = make_weights(g, E, K, N)
+    gate, up = (2 * normal(g, P, N)).to(BF), normal(g, P, N).to(BF)
+    q, s = torch.full((P, 2 * N), 9, dtype=torch.uint8, device="cuda"), torch.full((2 * N // 128, P), 7.0, device="cuda")
+    room = torch.empty(moe.fp8_block_glu_workspace_size(P, E, N, K, PRE), dtype=torch.uint8, device="cuda")
+    moe.fp8_block_glu_backward(moe.fp8_block_prepack_t(wq, ws), yq, ys, gate, up, off,
+                               **({"rows": pair, "row_div": 2} if gather else {}), flags=PRE, q=q, s=s, workspace=room)
+    assert_tall(room, name)
+    out = expert < 0
+    assert (q[out] == 9).all() and (s[:, out] == 7).all()
+    dy = ref.rows(yq, ys)
+    dy = dy[(pair // 2).long()] if gather else dy
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        if a < b:
+            dh, adh = ref.product(dy[a:b], ref.weights(wq[e], ws[e]).T.contiguous())
+            (dg, ag), (du, au) = ref.glu_grad(dh, adh, gate[a:b].double(), up[a:b].double())
+            v = ref.rows(q[a:b], s[:, a:b])
+            within(v[:, :N], dg, ref.held(dg, ag), f"dg, expert {e}")
+            within(v[:, N:], du, ref.held(du, au), f"du, expert {e}")
+
+
+@pytest.mark.parametrize("dtype", [BF, FS])
+@pytest.mark.parametrize("K", [2176, 8192])
+@pytest.mark.parametrize("T", [1, 8, 16])
+def test_dense_few_rows_of_many_tiles(T, K, dtype):
+    """More weight tiles than CUs and several K-steps in flight, with and without a remainder of them."""
+    N = 4128
+    g = gen(T + K)
+    xq, xs = make_rows(g, T, K)
+    wq, ws = make_weights(g, 1, N, K)
+    w = moe.fp8_block_prepack(wq[0], ws[0])
+    want, err = ref.product(ref.rows(xq, xs), ref.weights(wq[0], ws[0]), ref.HALF[dtype])
+    for flags in (0, DEC):
+        within(moe.fp8_block_dense(w, xq, xs, flags=flags, dtype=dtype), want, err)
+
+
+@pytest.mark.parametrize("flags", [0, DEC])
+def test_dense_fp32_of_a_few_hundred_rows(flags):
+    g = gen(333)
+    xq, xs = make_rows(g, 333, 4096)
+    wq, ws = make_weights(g, 1, 1536, 4096)
+    y = moe.fp8_block_dense(moe.fp8_block_prepack(wq[0], ws[0]), xq, xs, flags=flags, dtype=FS)
+    within(y, *ref.product(ref.rows(xq, xs), ref.weights(wq[0], ws[0])))
+
+
+@pytest.mark.parametrize("sizes", [[1, 0, 16, 7, 9, 2, 16, 16], [40, 0, 31, 17, 33, 64, 1, 25]])
+def test_streamed_groups_of_many_tiles(sizes):
+    """The products, the gated block and its backward pass: few rows a group and 16 of them or more on average, with
+    more weight tiles than CUs and several K-steps to a wave."""
+    E, P = len(sizes), sum(sizes)
+    K, N = 2176, 1152
+    g = gen(P)
+    off = torch.tensor([0] + sizes).cumsum(0).int().cuda()
+    xq, xs = make_rows(g, P, K)
+    (wq, ws), (uq, us) = make_weights(g, E, N, K), make_weights(g, E, N, K)
+    tq, ts = make_weights(g, E, K, N)
+    gate, up = (2 * normal(g, P, N)).to(BF), normal(g, P, N).to(BF)
+    w = moe.fp8_block_prepack(wq, ws)
+    sums = {t: moe.fp8_block_grouped(w, xq, xs, off, flags=DEC, dtype=t) for t in (BF, FS)}
+    hq, hs, hg, hu = moe.fp8_block_glu(moe.fp8_block_prepack_glu(wq, ws, uq, us), xq, xs, off, flags=DEC, save=True)
+    q, s = moe.fp8_block_glu_backward(moe.fp8_block_prepack_t(tq, ts), xq, xs, gate, up, off, flags=DEC)
+    x = ref.rows(xq, xs)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        if a == b:
+            continue
+        (vg, eg), (vu, eu), (h, eh) = ref.glu(x[a:b], ref.weights(wq[e], ws[e]), ref.weights(uq[e], us[e]))
+        for t, y in sums.items():
+            within(y[a:b], vg, eg + ref.HALF[t] * (vg.abs() + eg), f"{t}, expert {e}")
+        within(ref.rows(hq[a:b], hs[:, a:b]), h, ref.held(h, eh), f"h, expert {e}")
+        within(hg[a:b], vg, eg + ref.HALF[BF] * (vg.abs() + eg), "gate")
+        within(hu[a:b], vu, eu + ref.HALF[BF] * (vu.abs() + eu), "up")
+        dh, adh = ref.product(x[a:b], ref.weights(tq[e], ts[e]).T.contiguous())
+        (dg, ag), (du, au) = ref.glu_grad(dh, adh, gate[a:b].double(), up[a:b].double())
+        v = ref.rows(q[a:b], s[:, a:b])
+        within(v[:, :N], dg, ref.held(dg, ag), f"dg, expert {e}")
+        within(v[:, N:], du, ref.held(du, au), f"du, expert {e}")
+
+
+@pytest.mark.parametrize("dtype", [BF, FS])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("N,K", [(640, 2176), (384, 4480), (2304, 2048)])
+def test_weight_grad_of_several_panels(N, K, gather, dtype):
+    """More than eight tiles of columns of x: a narrow last panel, half tiles, tile counts that eight does not divide."""
+    sizes = [70, 0, 33, 1]
+    off = torch.tensor([2] + [2 + sum(sizes[:i + 1]) for i in range(4)], dtype=torch.int32, device="cuda")
+    P = 110
+    g = gen(N + K)
+    yq, ys = make_rows(g, P, N)
+    xq, xs = make_rows(g, P // 2 if gather else P, K)
+    pair = torch.randperm(P, generator=torch.Generator().manual_seed(1)).int().cuda()
+    dw = moe.fp8_block_weight_grad(yq, ys, xq, xs, off, **({"rows": pair, "row_div": 2} if gather else {}), dtype=dtype)
+    y, x = ref.rows(yq, ys), ref.rows(xq, xs)
+    if gather:
+        x, xs = x[(pair // 2).long()], xs[:, (pair // 2).long()]
+    for e in range(4):
+        a, b = int(off[e]), int(off[e + 1])
+        if a == b:
+            assert (dw[e] == 0).all()
+            continue
+        want, err = grad_bound(y[a:b], x[a:b], ref.HALF[dtype])
+        within(dw[e], want, err + row_floor(ys[:, a:b], xs[:, a:b]), f"expert {e}")
