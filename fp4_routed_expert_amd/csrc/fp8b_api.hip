@@ -41,31 +41,52 @@ moe_status_t check_weights(const moe_fp8_block_weights_t* w, int32_t glu) {
 // The tiled product addresses activation rows by 32-bit byte offsets.
 bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 << 32) - 4096; }
 
-// The rows up to which a call streams the weights by default: they are
-// streamed while the groups average at most 12 rows (us, streaming against tiled, 64
-// experts: SwiGLU K 4096 N 1536, 6 rows 119 and 142, 12 rows 145 and 146, 24 rows 181
-// and 148; 256 experts, K 7168 N 2048, 8 rows 1202 and 1277, 16 rows 1830 and 1320;
-// the backward call, 64 experts, K 4096 N 2048, 6 rows 86 and 102, 12 rows 90 and 102, 24
-// rows 111 and 104; 256 experts, K 7168 N 2048, 12 rows 619 and 644, 16 rows 665 and
-// 644), or while streaming makes at most 2048 passes of 32 rows over a weight tile,
-// eight per CU: the tiled product has few items then.  Dense: K 4096 N 1536, 512 rows (1536 passes) 20 and 27, 768 rows (2304) 30
-// and 27; K 16384 N 7168, 128 rows (1792) 80 and 120, 160 rows (2240) 125 and 116; K
-// 7168 N 2048, 512 rows (2048) 38 and 43.  Where the sums stay in fp32 up to 3584: K
-// 16384 N 7168, 256 rows (3584) 171 and 187; K 2048 N 7168, 256 rows 26 and 30, 333 rows
-// (4928) 33 and 31.  Grouped, where the tiled product lists its tiles
-// first, up to 2400 (a group's last pass counted half): 8 experts, K 512 N 512, 2048
-// rows (2176) 7.4 and 11.8; 16 experts, K 2048 N 512, 2000 rows (2240) 20 and 20; 30
-// experts, K 1024 N 1024, 1000 rows (2944) 14 and 14; 8 experts, K 4096 N 4096, 512
-// rows (5120) 67 and 32.
+// The rows up to which a call streams the weights by default (figures: us,
+// streaming against tiled).
+// - While the groups average at most 12 rows.  64 experts, SwiGLU K 4096 N 1536, 6 rows
+//   119 and 142, 12 rows 145 and 146, 24 rows 181 and 148; 256 experts, K 7168 N 2048, 8
+//   rows 1202 and 1277, 16 rows 1830 and 1320; the backward call, 64 experts, K 4096 N
+//   2048, 6 rows 86 and 102, 12 rows 90 and 102, 24 rows 111 and 104; 256 experts, K 7168
+//   N 2048, 12 rows 619 and 644, 16 rows 665 and 644.
+// - While streaming makes at most 2048 passes of 32 rows over a weight tile, eight per
+//   CU: the tiled product has few items then.  Dense: K 4096 N 1536, 512 rows (1536
+//   passes) 20 and 27, 768 rows (2304) 30 and 27; K 16384 N 7168, 128 rows (1792) 80 and
+//   120, 160 rows (2240) 125 and 116; K 7168 N 2048, 512 rows (2048) 38 and 43; K 512 N
+//   7168, 128 rows (1792) 6.8 and 9.0, 160 rows (2240) 9.0 and 9.0.
+// - Grouped, where the tiled product lists its tiles first, up to 2400 (a group's last
+//   pass counted half): 8 experts, K 512 N 512, 2272 rows (2400) 7.7 and 11.8; 30 experts,
+//   K 1024 N 1024, 704 rows (2368) 9.0 and 13.3, 992 rows (2944) 14.8 and 14.2; 16
+//   experts, K 2048 N 512, 2144 rows (2400) 21.0 and 19.6; 8 experts, K 4096 N 4096, 160
+//   rows (2304) 24 and 34, 320 rows (3584) 49 and 36.  Off by 10 % or more: 4 experts,
+//   K 7168 N 2048, 512 rows (2304) 59 and 46; 8 experts, K 4096 N 4096, 224 rows (2816)
+//   27 and 34; 8 and 64 experts, K 512, 2976 passes 10 and 12, 9 and 11.
+// - Where the sums stay in fp32 the tiled product is half as fast.  Dense, up to four
+//   rounds of the CUs of 64-row passes over a pair of tiles: K 4096 N 1536, 1344 rows (1008
+//   passes) 49 and 53, 1440 rows (1104) 60 and 53; K 16384 N 4096, 512 rows (1024) 171 and
+//   186, 544 rows (1152) 199 and 187; K 2048 N 2048, 1024 rows (1024) 24 and 30.  Half a
+//   round more for short K, whose workgroups overlap: K 1024 N 4096, 576 rows (1152) 16 and
+//   19; K 2048 N 7168, 288 rows (1120) 28 and 31, 352 rows (1344) 34 and 31; K 3584 N 7168,
+//   288 rows (1120) 48 and 47.  (Off by 10 % or more: K 256 N 1024, 2432 rows (1216)
+//   9.0 and 10.4; K 1024 N 4096, 608 rows (1280) 17.5 and 19.3.)
+// - Grouped in fp32 up to 3000 passes of 32 rows, for short K 4200: 4 experts, K 7168 N
+//   2048, 672 rows (2944) 89 and 88, 832 rows (3584) 111 and 89; 16 experts, K 2048 N 512,
+//   2720 rows (2976) 32 and 33, 3328 rows (3584) 39 and 33; 8 experts, K 512 N 512, 4064
+//   rows (4192) 10 and 16.5; 30 experts, K 1024 N 1024, 1600 rows (4160) 18 and 22.
 // The averages do not see skew, which only the device knows: streaming walks a
 // group's rows 16 or 32 at a time, by one workgroup per tile pair once the groups'
-// tiles fill the CUs.  A caller that knows its routing to be skewed forces the tiled
-// product.
+// tiles fill the CUs (64 experts, K 1536 N 4096, 512 rows in one of them: 58 and 18).  A
+// caller that knows its routing to be skewed forces the tiled product.
 int64_t streamed_rows(const Fp8bLayout& L, Fp8bOut out, bool grouped) {
-  const int64_t most = out == Fp8bOut::kFp32 ? 3584 : grouped ? 2400 : 2048;
-  // P / 32 + (E + 1) / 2 passes of groups, or P / 32 rounded up of one, times NT at most `most`
-  const int64_t passes = most / L.NT;
-  const int64_t few = grouped ? 32 * (passes - (L.E + 1) / 2) + 31 : 32 * passes;
+  const bool fp32 = out == Fp8bOut::kFp32;
+  int64_t few;
+  if (grouped) {  // P / 32 + (E + 1) / 2 passes, times NT
+    const int64_t most = !fp32 ? 2400 : L.K < 2048 ? 4200 : 3000;
+    few = 32 * (most / L.NT - (L.E + 1) / 2) + 31;
+  } else if (fp32) {
+    few = 64 * ((L.K <= 2048 ? 1152 : 1024) / (L.NT / 2));
+  } else {
+    few = 32 * (2048 / L.NT);
+  }
   return few > 12 * L.E ? few : 12 * L.E;
 }
 
