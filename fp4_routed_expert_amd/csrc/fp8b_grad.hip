@@ -91,22 +91,12 @@ __global__ __launch_bounds__(1024) void entries_kernel(Fp8bGradArgs a, int32_t* 
   if (p < a.P) xrows[p] = entry_row(a.rows, p, a.div, a.X);
 }
 
-// LDS-DMA of 16 bytes, or a dword, for each lane from an address of its own.
+// LDS-DMA of 16 bytes for each lane from an address of its own.
 __device__ __forceinline__ void dma16_lanes(const uint8_t* p, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %1\n\t"
       "s_nop 0\n\t"
       "global_load_lds_dwordx4 %0, off"
-      :
-      : "v"(p), "s"(wave_u32(lds))
-      : "memory");
-}
-
-__device__ __forceinline__ void dma4_from(const uint8_t* p, uint32_t lds) {
-  asm volatile(
-      "s_mov_b32 m0, %1\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dword %0, off"
       :
       : "v"(p), "s"(wave_u32(lds))
       : "memory");
@@ -183,7 +173,7 @@ __device__ __forceinline__ void run_rows(const GradCtx& g, v16f (&acc)[4][2]) {
     if constexpr (!kIsX) {
       const uint32_t to = lds0 + (uint32_t)(kOffScale + 1024 * slot + 256 * o);
       if (kGather && o >= 2)
-        dma4_from(reinterpret_cast<const uint8_t*>(g.scales + entry(step, lane & 31)), to);
+        dma4_lanes(reinterpret_cast<const uint8_t*>(g.scales + entry(step, lane & 31)), to);
       else
         dma4(reinterpret_cast<const uint8_t*>(g.scales + first_of(step)), scale_off, to);
     }

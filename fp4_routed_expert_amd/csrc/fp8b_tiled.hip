@@ -207,17 +207,6 @@ struct Ctx {
   }
 };
 
-// LDS-DMA of a dword for each lane from an address of its own.
-__device__ __forceinline__ void dma4_lanes(const uint8_t* p, uint32_t lds) {
-  asm volatile(
-      "s_mov_b32 m0, %1\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dword %0, off"
-      :
-      : "v"(p), "s"(wave_u32(lds))
-      : "memory");
-}
-
 // Token tiles that wave row wm (of four) takes of a tile of n rows: how many, and
 // the first one.  Wave rows 0 and 2 share SIMDs, as do 1 and 3.
 __device__ __forceinline__ int sub_tiles(int n, int wm) { return ((n + 15) / 16 + 3 - wm) / 4; }
@@ -793,9 +782,10 @@ hipError_t launch_fp8b_tiled(const Fp8bArgs& a, const Fp8bLayout& L, Fp8bOut out
   const int ntn = (L.NT + kBT - 1) / kBT;
   const int most = out == Fp8bOut::kFp32 ? kWideSubs : 4;
   // Where a group is a tile on average its weights are read once whatever the walk, and
-  // one panel keeps its rows in L2 (us, one panel and four, 256 experts of 144 rows, K
-  // 7168, N 2048: SwiGLU 1560 and 1570, its backward pass 889 and 894; 64 experts of 96
-  // rows, K 4096, N 1536, 151 and 155); else panels share weights between row tiles
+  // one panel keeps its rows in L2 (us, one panel and four, three runs in turn: 256
+  // experts of 144 rows, K 7168, N 2048, SwiGLU 1548 and 1559, its backward pass 849 and
+  // 863, K 2048, N 7168 806 and 816; 64 experts of 96 rows, K 4096, N 1536, SwiGLU 153 and
+  // 158, but K 1536, N 4096, 102 and 99); else panels share weights between row tiles
   // (T16384 to 256 experts, skewed, K 2048, N 7168: 2338 and 2165; dense, 4604 rows, K
   // 16384, N 7168, 455 and 437; two, six, seven, eight and fourteen panels 0-5 % slower).
   Launch g{a, L, nullptr, nullptr, 0, 0, a.offsets && a.P <= kBM * (long)L.E ? 1 : 4};

@@ -57,6 +57,17 @@ __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t
       : "memory");
 }
 
+// LDS-DMA of a dword for each lane from an address of its own.
+__device__ __forceinline__ void dma4_lanes(const uint8_t* p, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %0, off"
+      :
+      : "v"(p), "s"(wave_u32(lds))
+      : "memory");
+}
+
 // Where a wave's walk over the items stands (in LDS between items).  The items
 // go by panels of columns (a quarter of them), row tiles running inside a panel,
 // so that the items that an XCD holds at one time share rows and weights in
