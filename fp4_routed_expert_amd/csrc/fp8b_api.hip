@@ -45,9 +45,11 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 
 // streaming against tiled).
 // - While the groups average at most 12 rows.  64 experts, SwiGLU K 4096 N 1536, 6 rows
 //   119 and 142, 12 rows 145 and 146, 24 rows 181 and 148; 256 experts, K 7168 N 2048, 8
-//   rows 1202 and 1277, 16 rows 1830 and 1320; the backward call, 64 experts, K 4096 N
-//   2048, 6 rows 86 and 102, 12 rows 90 and 102, 24 rows 111 and 104; 256 experts, K 7168
-//   N 2048, 12 rows 619 and 644, 16 rows 665 and 644.
+//   rows 1202 and 1277, 16 rows 1830 and 1320.  The backward call 6 rows: evenly routed
+//   it gains up to 12 (64 experts, K 4096 N 2048, 6 rows 84 and 100, 8 rows 88 and 102, 12
+//   rows 103 and 102; 256 experts, K 7168 N 2048, 7 rows 579 and 638, 12 rows 663 and 645),
+//   but skewed by Zipf's law it loses more (8 rows on average 96 and 78, 12 rows 128 and
+//   78; 256 experts, 7 rows 425 and 209, 12 rows 718 and 244).
 // - While streaming makes at most 2048 passes of 32 rows over a weight tile, eight per
 //   CU: the tiled product has few items then.  Dense: K 4096 N 1536, 512 rows (1536
 //   passes) 20 and 27, 768 rows (2304) 30 and 27; K 16384 N 7168, 128 rows (1792) 80 and
@@ -68,10 +70,11 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 
 //   19; K 2048 N 7168, 288 rows (1120) 28 and 31, 352 rows (1344) 34 and 31; K 3584 N 7168,
 //   288 rows (1120) 48 and 47.  (Off by 10 % or more: K 256 N 1024, 2432 rows (1216)
 //   9.0 and 10.4; K 1024 N 4096, 608 rows (1280) 17.5 and 19.3.)
-// - Grouped in fp32 up to 3000 passes of 32 rows, for short K 4200: 4 experts, K 7168 N
+// - Grouped in fp32 up to 3000 passes of 32 rows, for short K 3584: 4 experts, K 7168 N
 //   2048, 672 rows (2944) 89 and 88, 832 rows (3584) 111 and 89; 16 experts, K 2048 N 512,
-//   2720 rows (2976) 32 and 33, 3328 rows (3584) 39 and 33; 8 experts, K 512 N 512, 4064
-//   rows (4192) 10 and 16.5; 30 experts, K 1024 N 1024, 1600 rows (4160) 18 and 22.
+//   2720 rows (2976) 32 and 33, 3328 rows (3584) 39 and 33; 8 experts, K 512 N 512, 3456
+//   rows (3584) 9.4 and 16.3; 30 experts, K 1024 N 1024, 1312 rows (3584) 17 and 21.  (Evenly
+//   routed short K gains up to 4200 passes, 10 and 16.5, 18 and 22; skewed it would not.)
 // The averages do not see skew, which only the device knows: streaming walks a
 // group's rows 16 or 32 at a time, by one workgroup per tile pair once the groups'
 // tiles fill the CUs (64 experts, K 1536 N 4096, 512 rows in one of them: 58 and 18).  A
@@ -80,14 +83,15 @@ int64_t streamed_rows(const Fp8bLayout& L, Fp8bOut out, bool grouped) {
   const bool fp32 = out == Fp8bOut::kFp32;
   int64_t few;
   if (grouped) {  // P / 32 + (E + 1) / 2 passes, times NT
-    const int64_t most = !fp32 ? 2400 : L.K < 2048 ? 4200 : 3000;
+    const int64_t most = !fp32 ? 2400 : L.K < 2048 ? 3584 : 3000;
     few = 32 * (most / L.NT - (L.E + 1) / 2) + 31;
   } else if (fp32) {
     few = 64 * ((L.K <= 2048 ? 1152 : 1024) / (L.NT / 2));
   } else {
     few = 32 * (2048 / L.NT);
   }
-  return few > 12 * L.E ? few : 12 * L.E;
+  const int64_t rows = (out == Fp8bOut::kGluGrad ? 6 : 12) * (int64_t)L.E;
+  return few > rows ? few : rows;
 }
 
 // 0: stream the weights, 1: tiled, -1: bad flags.
