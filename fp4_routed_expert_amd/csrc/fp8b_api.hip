@@ -68,7 +68,10 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 
 //   186, 544 rows (1152) 199 and 187; K 2048 N 2048, 1024 rows (1024) 24 and 30.  Half a
 //   round more for short K, whose workgroups overlap: K 1024 N 4096, 576 rows (1152) 16 and
 //   19; K 2048 N 7168, 288 rows (1120) 28 and 31, 352 rows (1344) 34 and 31; K 3584 N 7168,
-//   288 rows (1120) 48 and 47.  (Off by 10 % or more: K 256 N 1024, 2432 rows (1216)
+//   288 rows (1120) 48 and 47.  Or at most 3584 passes of 32 rows, where half of a last
+//   one of 64 would be empty: K 4096, N 36864, 32 rows (2304) 36 and 40, N 11264, 160 rows
+//   (3520) 49 and 53, N 18432, 96 rows (3456) 50 and 52, N 48000, 32 rows (3000) 44 and
+//   43.  (Off by 10 % or more: K 4096 N 57344, 32 rows (3584) 51 and 46; K 256 N 1024, 2432 rows (1216)
 //   9.0 and 10.4; K 1024 N 4096, 608 rows (1280) 17.5 and 19.3.)
 // - Grouped in fp32 up to 3000 passes of 32 rows, for short K 3584: 4 experts, K 7168 N
 //   2048, 672 rows (2944) 89 and 88, 832 rows (3584) 111 and 89; 16 experts, K 2048 N 512,
@@ -86,7 +89,8 @@ int64_t streamed_rows(const Fp8bLayout& L, Fp8bOut out, bool grouped) {
     const int64_t most = !fp32 ? 2400 : L.K < 2048 ? 3584 : 3000;
     few = 32 * (most / L.NT - (L.E + 1) / 2) + 31;
   } else if (fp32) {
-    few = 64 * ((L.K <= 2048 ? 1152 : 1024) / (L.NT / 2));
+    const int64_t wide = 64 * ((L.K <= 2048 ? 1152 : 1024) / (L.NT / 2)), narrow = 32 * (3584 / L.NT);
+    few = wide > narrow ? wide : narrow;
   } else {
     few = 32 * (2048 / L.NT);
   }
