@@ -996,3 +996,19 @@ def test_weight_grad_of_several_panels(N, K, gather, dtype):
             continue
         want, err = grad_bound(y[a:b], x[a:b], ref.HALF[dtype])
         within(dw[e], want, err + row_floor(ys[:, a:b], xs[:, a:b]), f"expert {e}")
+
+
+@pytest.mark.parametrize("flags", [0, DEC, PRE])
+@pytest.mark.parametrize("T,K,N", [(1, 256, 256), (20, 384, 640), (33, 2176, 128), (128, 256, 4096), (300, 128, 384)])
+def test_glu_backward_without_groups(flags, T, K, N):
+    """One group, as a shared expert has; 128 rows of 256 weight tiles are streamed 64 rows a pass."""
+    g = gen(T + K)
+    yq, ys = make_rows(g, T, K)
+    wq, ws = make_weights(g, 1, K, N)
+    gate, up = (2 * normal(g, T, N)).to(BF), normal(g, T, N).to(BF)
+    q, s = moe.fp8_block_glu_backward(moe.fp8_block_prepack_t(wq[0], ws[0]), yq, ys, gate, up, flags=flags)
+    dh, adh = ref.product(ref.rows(yq, ys), ref.weights(wq[0], ws[0]).T.contiguous())
+    (dg, ag), (du, au) = ref.glu_grad(dh, adh, gate.double(), up.double())
+    v = ref.rows(q, s)
+    within(v[:, :N], dg, ref.held(dg, ag), "dg")
+    within(v[:, N:], du, ref.held(du, au), "du")
