@@ -71,8 +71,8 @@ bool rows_too_large(int32_t X, int32_t K) { return (int64_t)X * K > ((int64_t)1 
 //   288 rows (1120) 48 and 47.  Or at most 3584 passes of 32 rows, where half of a last
 //   one of 64 would be empty: K 4096, N 36864, 32 rows (2304) 36 and 40, N 11264, 160 rows
 //   (3520) 49 and 53, N 18432, 96 rows (3456) 50 and 52, N 48000, 32 rows (3000) 44 and
-//   43.  (Off by 10 % or more: K 4096 N 57344, 32 rows (3584) 51 and 46; K 256 N 1024, 2432 rows (1216)
-//   9.0 and 10.4; K 1024 N 4096, 608 rows (1280) 17.5 and 19.3.)
+//   43.  (Off by 10 % or more: K 4096 N 57344, 32 rows (3584) 51 and 46; K 256 N 1024,
+//   2432 rows (1216) 9.0 and 10.4; K 1024 N 4096, 608 rows (1280) 17.5 and 19.3.)
 // - Grouped in fp32 up to 3000 passes of 32 rows, for short K 3584: 4 experts, K 7168 N
 //   2048, 672 rows (2944) 89 and 88, 832 rows (3584) 111 and 89; 16 experts, K 2048 N 512,
 //   2720 rows (2976) 32 and 33, 3328 rows (3584) 39 and 33; 8 experts, K 512 N 512, 3456
@@ -315,7 +315,8 @@ moe_status_t moe_fp8_block_weight_grad(const uint8_t* yq, const float* ys, const
   if (P < 0 || X < 0 || row_div < 1 || !sum_type(dw_type)) return MOE_ERR_INVALID_ARGUMENT;
   // one workgroup of 512 threads per 256 x 256 outputs (a last tile may be half of one), in multiples of eight:
   // below 2^32 threads
-  if (N % 128 != 0 || P > kMaxP || (int64_t)((N + 255) / 256) * ((K + 255) / 256) > (1 << 23) - 8) return MOE_ERR_UNSUPPORTED;
+  const int64_t tiles = (int64_t)((N + 255) / 256) * ((K + 255) / 256);
+  if (N % 128 != 0 || P > kMaxP || tiles > (1 << 23) - 8) return MOE_ERR_UNSUPPORTED;
   if (!dw || !aligned(dw, 16)) return MOE_ERR_INVALID_ARGUMENT;
   if (P > 0) {
     st = check_rows(X, offsets, rows, P, E);

@@ -197,7 +197,8 @@ def fp8_block_glu(w: Fp8BlockWeights, xq: torch.Tensor, xs: torch.Tensor, offset
                   up: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Quantised rows of h = silu(gate) * up, gate = x W1^T and up = x W3^T: (q [P, N], s [N/128, P], gate, up).
     gate and up [P, N] bf16 are kept for the backward pass with ``save`` or where given, else None.  Rows and
-    groups as for fp8_block_grouped; without ``offsets`` one group."""
+    groups as for fp8_block_grouped; without ``offsets`` (and ``rows``) one group.  A workspace for the largest P
+    serves every smaller one, and the backward call."""
     _form(w, True, "fp8_block_glu")
     X, dev = xq.shape[0], xq.device
     P = X if rows is None else rows.shape[0]
@@ -244,8 +245,8 @@ def fp8_block_weight_grad(yq: torch.Tensor, ys: torch.Tensor, xq: torch.Tensor, 
                           dtype: torch.dtype = torch.bfloat16, dw: torch.Tensor | None = None,
                           workspace: torch.Tensor | None = None):
     """dw [E, N, K] (bf16 or fp32): the sum over group e's rows s of dy[s]^T x[r], r as for fp8_block_grouped, from
-    quantised rows (yq [P, N], ys [N/128, P]; xq [X, K], xs [K/128, X]).  Without ``offsets`` one group, dw [N, K]
-    or [1, N, K].  A group without rows gets zeros."""
+    quantised rows (yq [P, N], ys [N/128, P]; xq [X, K], xs [K/128, X]).  Without ``offsets`` (and ``rows``) one
+    group, dw [N, K] or [1, N, K].  A group without rows gets zeros."""
     if yq.dim() != 2 or xq.dim() != 2:
         raise ValueError(f"yq, xq: shapes {tuple(yq.shape)}, {tuple(xq.shape)}, not [P, N] and [X, K]")
     (P, N), (X, K) = yq.shape, xq.shape

@@ -156,8 +156,9 @@ moe_status_t moe_fp8_block_glu_forward(const moe_fp8_block_weights_t* w /*(host)
  * as above: dh[s] = W2[e]^T dO[r(s)], sig = 1 / (1 + e^-g),
  *   dg = dh u sig (1 + g (1 - sig)),  du = dh g sig
  * in fp32 (sig from the hardware's exponential and reciprocal; 0 below g = -87.3,
- * where |g| sig < 2^-118), quantised in blocks of 128 of each.  [dg, du] are the rows of the input gradient's product
- * (moe_fp8_block_prepack_t of both projections) and of the weight gradient.
+ * where |g| sig < 2^-118), quantised in blocks of 128 of each.  [dg, du] are the
+ * rows of the input gradient's product (moe_fp8_block_prepack_t of both
+ * projections) and of the weight gradient.
  *   w plain, from moe_fp8_block_prepack_t of W2 [E, K, N]: N the block's inner
  *     width, N % 128 == 0
  *   yq [X, K], ys [K/128, X]: the rows dO
@@ -182,7 +183,7 @@ moe_status_t moe_fp8_block_glu_backward(const moe_fp8_block_weights_t* w /*(host
  * Sums in fp32, rounded once to dw_type (bf16, or fp32 as it is).  A group without
  * rows gets zeros.
  *   yq [P, N], ys [N/128, P]; xq [X, K], xs [K/128, X]; codes 16-byte aligned
- *   offsets null: one group of P rows (E == 1); rows as above
+ *   offsets null, then rows too: one group of P rows (E == 1); else as above
  *   dw [E, N, K] (out, 16-byte aligned); N % 128 == 0, K % 128 == 0
  *   workspace >= moe_fp8_block_weight_grad_workspace_size(P, E, N, K) bytes,
  *     256-byte aligned, as above
